@@ -315,6 +315,150 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
                                void *stream);
 
 /*
+ * ---- Softmax attention for the other layers of a hybrid stack -------------
+ *
+ * Stacks that keep a few full-attention layers between linear ones (the
+ * knowledge-base page's section 4 and the concept card's "When to use which"
+ * describe them) need, next to the calls above, causal softmax attention over
+ * the prompt, a key/value cache with a decode step over it, and a way to bound
+ * that cache.  The conventions at the top of this file hold, except as
+ * stated: q has H heads, k and v have H_kv, H a multiple of H_kv; query head h
+ * reads key/value head h / (H / H_kv).  d in {32, 64, 128}, in_dtype F32,
+ * BF16 or F16, out_dtype == in_dtype or LA_F32.
+ *
+ * Packed sequences: N tokens of n_seq sequences lie behind one another;
+ * cu_seqlens (device, n_seq + 1 int32, non-decreasing, from 0 on) says where
+ * each begins: sequence s is tokens [cu_seqlens[s], cu_seqlens[s + 1]).  A
+ * sequence may be empty.  Tokens from cu_seqlens[n_seq] on belong to none:
+ * they are not read for any other and their output rows are left as they were.
+ * The values are read on the device only and clamped to [0, N].
+ *
+ * Strides: host arrays of (head, token) pairs in elements, NULL for contiguous
+ * [heads, N, d]; the channels of a token are contiguous.  Every stride of an
+ * extent above 1 is at least d, a multiple of 16 bytes and below 2^39 bytes;
+ * else LA_ERR_INVALID_ARG.
+ */
+
+/*
+ * la_softmax_prefill — causal softmax attention over a packed prompt:
+ *   out_i = sum_{j <= i, same sequence} p_ij v_j,
+ *   p_ij = exp(scale q_i.k_j) / sum_{j' <= i} exp(scale q_i.k_j')
+ *   q, out [H, N, d], k, v [H_kv, N, d]; strides: 8 entries (q, k, v, out)
+ *   scale  finite and > 0
+ *   out    must not overlap the inputs
+ * Keys and values behind a query, or of another sequence, do not reach it,
+ * not even as NaN or infinity.  Sums and the running maximum are fp32; with
+ * 16-bit inputs at d 64 or 128 (the tensor-core kernel) the unnormalised
+ * weights, which lie in [0, 1], are rounded once to the input type for the
+ * product with v.
+ * The workspace (la_softmax_prefill_workspace_size bytes, 256-byte aligned)
+ * starts with the status word that la_workspace_status reads.
+ */
+la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dtype in_dtype, int H, int H_kv,
+                             int N, int d, const int32_t *cu_seqlens, int n_seq, const int64_t *strides,
+                             float scale, void *out, la_dtype out_dtype, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace la_softmax_prefill needs (0 for sizes it refuses). */
+size_t la_softmax_prefill_workspace_size(int H, int H_kv, int N, int d, int n_seq);
+
+/*
+ * A key/value cache in 4 bits: B sequences, H_kv heads, room for `cap`
+ * positions each.  The four arrays are the caller's, contiguous and 16-byte
+ * aligned:
+ *   k_codes, v_codes  [B, H_kv, cap, d / 2] bytes
+ *   k_par, v_par      [B, H_kv, cap, d / 32] 32-bit words
+ * A row (one position of one head) is cut into groups of 32 channels.  A
+ * group's word holds a bf16 scale in its low and an fp16 offset in its high
+ * half; the value of a channel with code c is scale * (c + offset).  A row's
+ * bytes are 8 chunks of d / 16 bytes; chunk r holds for each group g, as
+ * little-endian 16-bit field g, the codes of channels 32 g + 4 r + {0,1,2,3},
+ * the first in the lowest four bits.
+ * Quantisation of a group x (float64 arithmetic; a rounding to 16 bits goes
+ * through fp32, to nearest even each time):
+ *   scale  = bf16(max((max x - min x) / 15, max |x| / 1024))
+ *   offset = fp16(min x / scale)
+ *   code   = clamp(rint(x / scale - offset), 0, 15)
+ * (the second bound on scale keeps the offset in fp16's exact range when a
+ * group varies little around a large value; what it loses is below the
+ * resolution of a 16-bit input).  scale 0: every value is 0.  A group with
+ * NaN or an infinity gets scale NaN: all its values read back as NaN.
+ */
+typedef struct {
+    uint8_t *k_codes;
+    uint32_t *k_par;
+    uint8_t *v_codes;
+    uint32_t *v_par;
+    int B, H_kv, cap, d;
+} la_kv4_cache;
+
+/*
+ * la_kv4_append — writes tokens' keys and values into the cache.  Token t of
+ * sequence s (the packed layout above, n_seq == cache->B) goes to position
+ * start[s] + (t - cu_seqlens[s]) of sequence s; positions outside [0, cap) are
+ * dropped.  cu_seqlens NULL: one token per sequence (N == cache->B).
+ *   k, v   [H_kv, N, d] in_dtype; strides: 4 entries (k, v)
+ *   start  [B] int32, device
+ * Two tokens never share a position of one call; the cache keeps no lengths.
+ */
+la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, const int64_t *strides,
+                        const int32_t *cu_seqlens, const int32_t *start, const la_kv4_cache *cache,
+                        void *stream);
+
+/*
+ * la_kv4_read — the inverse: the values of positions start[s] + (t -
+ * cu_seqlens[s]), as k_out, v_out [H_kv, N, d] out_dtype, contiguous.
+ * Positions outside [0, cap) and tokens of no sequence give zeros.
+ */
+la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlens, const int32_t *start,
+                      void *k_out, void *v_out, la_dtype out_dtype, void *stream);
+
+/*
+ * la_kv4_decode — softmax attention of one query token per sequence over the
+ * cache's first lens[b] positions (lens [B] int32, device, clamped to
+ * [0, cap]; a length of 0 gives zeros):
+ *   out[b,h] = sum_t p_t V[b,h',t],  p = softmax_t(scale q[b,h].K[b,h',t])
+ *   q, out  [B, H, d] contiguous
+ *   weights_out  [B, H_kv, cap] fp32 or NULL: for t < lens[b] receives
+ *           weights_in (zeros if NULL) + the sum of p_t over the query heads
+ *           of that key/value head; the other entries are left as they were.
+ *           May be weights_in itself; must not overlap it otherwise.
+ * The products run on the tensor cores in 16-bit terms: 4-bit codes are exact
+ * there, 16-bit queries too; fp32 queries are carried as three bf16 terms and
+ * the weights times the values' scales as one term of the query's type
+ * (fp32: two bf16 terms).  Sums are fp32.
+ */
+la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_cache *cache, const int32_t *lens,
+                        float scale, const float *weights_in, float *weights_out, void *out,
+                        la_dtype out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace la_kv4_decode needs (with_weights: whether weights_out
+ * is given; 0 for sizes it refuses). */
+size_t la_kv4_decode_workspace_size(int B, int H, int H_kv, int cap, int d, int with_weights);
+
+/*
+ * la_kv4_evict — cuts every (sequence, head) of a cache down to `keep`
+ * positions: the `recent` newest and, of the others, those with the greatest
+ * weight (ties to the lower position; NaN counts as greater than any number).
+ * With lens[b] <= keep all are kept.  The kept rows go, in their order, to the
+ * first positions of `out`, another cache of the same B, H_kv and d with
+ * out->cap >= keep, whose buffers must not overlap the cache's; rows behind
+ * them are left as they were.
+ *   weights      [B, H_kv, cap] fp32 (see la_kv4_decode)
+ *   lens         [B] int32, device, clamped to [0, cap]
+ *   0 <= recent <= keep, keep >= 1
+ *   out_weights  [B, H_kv, out->cap] fp32 or NULL: the kept positions' weights
+ *   kept         [B, H_kv, keep] int32 or NULL: their old positions, -1 behind them
+ *   out_lens     [B] int32 or NULL: min(lens[b], keep)
+ */
+la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const int32_t *lens, int keep,
+                       int recent, const la_kv4_cache *out, float *out_weights, int32_t *kept,
+                       int32_t *out_lens, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace la_kv4_evict needs (0 for sizes it refuses). */
+size_t la_kv4_evict_workspace_size(int B, int H_kv, int cap, int keep);
+
+/*
  * Status of the last call that used `workspace` (a workspace passed to
  * la_prefill_causal*, la_forward_noncausal or la_prefill_causal_noalloc's
  * array): LA_OK, or LA_ERR_TIMEOUT if a bounded device-side wait of that call

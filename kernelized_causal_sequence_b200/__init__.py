@@ -10,6 +10,11 @@ the C ABI's names (``include/linattn.h``):
     la_forward_noncausal(q, k, v, eps=1e-6, ...)
     la_decode_step(q, k, v, state_S, state_z, decay=None, eps=1e-6, ...)
 
+and, for the softmax layers of a hybrid stack,
+
+    la_softmax_prefill(q, k, v, cu_seqlens, ...)
+    la_kv4_append / la_kv4_read / la_kv4_decode / la_kv4_evict on a KV4Cache
+
 If the shared library has not been built, importing works but every call
 raises: there is no fallback of any kind.
 """
@@ -17,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -27,6 +33,8 @@ __all__ = [
     "la_prefill_workspace_size", "la_noncausal_workspace_size", "la_status_string",
     "la_prefill_path", "la_launch_count", "la_workspace_status", "la_set_wait_limit_ns", "LA_F32", "LA_BF16", "LA_F16", "LA_STATE_NONE", "LA_STATE_OUT",
     "LA_STATE_INOUT", "LIB_PATH",
+    "KV4Cache", "la_softmax_prefill", "la_kv4_append", "la_kv4_read", "la_kv4_decode", "la_kv4_evict",
+    "la_softmax_prefill_workspace_size", "la_kv4_decode_workspace_size", "la_kv4_evict_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblinattn.so")
@@ -39,6 +47,11 @@ _DT = {torch.float32: LA_F32, torch.bfloat16: LA_BF16, torch.float16: LA_F16}
 
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+
+
+class _Kv4CacheC(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_par", _vp), ("v_codes", _vp), ("v_par", _vp), ("B", _i), ("H_kv", _i),
+                ("cap", _i), ("d", _i)]
 
 
 class LinAttnError(RuntimeError):
@@ -111,6 +124,23 @@ def lib() -> ctypes.CDLL:
         L.la_noalloc_status.argtypes = [ctypes.POINTER(_i), _vp]
         L.la_set_wait_limit_ns.restype = ctypes.c_uint64
         L.la_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
+        _cp = ctypes.POINTER(_Kv4CacheC)
+        L.la_softmax_prefill.restype = _i
+        L.la_softmax_prefill.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _f, _vp, _i, _vp, _sz, _vp]
+        L.la_softmax_prefill_workspace_size.restype = _sz
+        L.la_softmax_prefill_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+        L.la_kv4_append.restype = _i
+        L.la_kv4_append.argtypes = [_vp, _vp, _i, _i, _vp, _vp, _vp, _cp, _vp]
+        L.la_kv4_read.restype = _i
+        L.la_kv4_read.argtypes = [_cp, _i, _vp, _vp, _vp, _vp, _i, _vp]
+        L.la_kv4_decode.restype = _i
+        L.la_kv4_decode.argtypes = [_vp, _i, _i, _cp, _vp, _f, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+        L.la_kv4_decode_workspace_size.restype = _sz
+        L.la_kv4_decode_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+        L.la_kv4_evict.restype = _i
+        L.la_kv4_evict.argtypes = [_cp, _vp, _vp, _i, _i, _cp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.la_kv4_evict_workspace_size.restype = _sz
+        L.la_kv4_evict_workspace_size.argtypes = [_i, _i, _i, _i]
         _lib = L
     return _lib
 
@@ -350,3 +380,281 @@ def la_decode_step(q, k, v, state_S, state_z, decay=None, eps=1e-6, out=None, ou
                                     _DT[out.dtype], _stream(stream))
     _check("la_decode_step_gated" if gain is not None else "la_decode_step", st)
     return out
+
+
+# ---- softmax attention for the other layers of a hybrid stack --------------
+#
+# These functions check what the C ABI cannot see (shapes, types, devices) and
+# raise ValueError before anything is launched.  A call runs on ``stream``, or
+# on the current stream of its tensors' device.
+
+class KV4Cache(typing.NamedTuple):
+    """A key/value cache in 4 bits (the format: la_kv4_cache in linattn.h).
+
+    k_codes, v_codes: [B, H_kv, cap, d / 2] uint8; k_par, v_par:
+    [B, H_kv, cap, d / 32] int32; contiguous, on one device."""
+    k_codes: torch.Tensor
+    k_par: torch.Tensor
+    v_codes: torch.Tensor
+    v_par: torch.Tensor
+
+    @classmethod
+    def alloc(cls, B, H_kv, cap, d, device="cuda"):
+        """An uninitialised cache for B sequences, H_kv heads of d channels and
+        ``cap`` positions."""
+        def half():
+            return (torch.empty((B, H_kv, cap, d // 2), dtype=torch.uint8, device=device),
+                    torch.empty((B, H_kv, cap, d // 32), dtype=torch.int32, device=device))
+        return cls(*half(), *half())
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _cache_c(cache, what="cache"):
+    kc, kp, vc, vp = cache
+    _need(kc.dim() == 4 and kc.dtype == torch.uint8 and kc.is_cuda, f"{what}.k_codes: [B, H_kv, cap, d / 2] uint8 on CUDA")
+    B, Hk, cap, half = kc.shape
+    d = half * 2
+    _need(d in (32, 64, 128), f"{what}: head dim 32, 64 or 128, not {d}")
+    _need(vc.shape == kc.shape and vc.dtype == torch.uint8, f"{what}.v_codes: as k_codes")
+    for x in (kp, vp):
+        _need(x.dtype == torch.int32 and tuple(x.shape) == (B, Hk, cap, d // 32), f"{what}: k_par, v_par [B, H_kv, cap, d / 32] int32")
+    for x in cache:
+        _need(x.device == kc.device and x.is_contiguous(), f"{what}: contiguous tensors on one device")
+    return _Kv4CacheC(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, Hk, cap, d)
+
+
+def _ints(x, n, device, what):
+    _need(x.dtype == torch.int32 and x.dim() == 1 and x.device == device and x.is_contiguous()
+          and (n is None or x.numel() == n), f"{what}: contiguous int32" + ("" if n is None else f" [{n}]") + f" on {device}")
+
+
+def _packed(x, like, heads, what):
+    # a [heads, N, d] view whose channels are contiguous
+    _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] == 1), f"{what}: [heads, N, d] with contiguous channels")
+    if like is not None:
+        _need(x.dtype == like.dtype and x.device == like.device and x.shape[1:] == like.shape[1:]
+              and (heads is None or x.shape[0] == heads), f"{what}: does not match the other inputs")
+
+
+def _strides(*xs):
+    return (ctypes.c_int64 * (2 * len(xs)))(*[s for x in xs for s in x.stride()[:2]])
+
+
+class _On:
+    """The device and stream of one call.  With a stream other than the
+    current one, what the call allocates comes from that stream's memory, and
+    the caching allocator is told of every tensor that both streams touch."""
+
+    def __init__(self, device, stream):
+        self.current = torch.cuda.current_stream(device)
+        self.stream = self.current if stream is None else stream
+        self.other = self.stream.cuda_stream != self.current.cuda_stream
+        _need(self.stream.device == device, "stream: of another device than the tensors")
+        self.guard = None
+        if self.other:
+            self.guard = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    @property
+    def ptr(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def uses(self, *given):
+        """Tensors of the caller that this call reads or writes."""
+        if self.other:
+            for x in given:
+                if x is not None:
+                    x.record_stream(self.stream)
+
+    def hands(self, *made):
+        """Tensors that this call allocated for the caller."""
+        if self.other:
+            for x in made:
+                x.record_stream(self.current)
+
+
+def la_softmax_prefill_workspace_size(H, H_kv, N, d, n_seq) -> int:
+    return int(lib().la_softmax_prefill_workspace_size(H, H_kv, N, d, n_seq))
+
+
+def la_kv4_decode_workspace_size(B, H, H_kv, cap, d, with_weights=False) -> int:
+    return int(lib().la_kv4_decode_workspace_size(B, H, H_kv, cap, d, int(bool(with_weights))))
+
+
+def la_kv4_evict_workspace_size(B, H_kv, cap, keep) -> int:
+    return int(lib().la_kv4_evict_workspace_size(B, H_kv, cap, keep))
+
+
+def _ws(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    _need(workspace.device == device and workspace.is_contiguous(), f"workspace: contiguous, on {device}")
+    return workspace
+
+
+def la_softmax_prefill(q, k, v, cu_seqlens, scale=None, out=None, out_dtype=None, workspace=None, stream=None):
+    """Causal softmax attention over a packed prompt with grouped heads.
+
+    q: [H, N, d]; k, v: [H_kv, N, d] (f32/bf16/f16, views with any head and
+    token strides that are multiples of 16 bytes); cu_seqlens: [n_seq + 1]
+    int32 on the device, sequence s being tokens cu_seqlens[s] ..
+    cu_seqlens[s + 1] - 1.  ``scale`` defaults to d ** -0.5.  Returns ``out``
+    [H, N, d]; its rows behind the last sequence are left as they were."""
+    _packed(q, None, None, "q")
+    _need(q.is_cuda and q.dtype in _DT, "q: f32, bf16 or f16 on CUDA")
+    H, N, d = q.shape
+    _packed(k, q, None, "k")
+    _packed(v, q, k.shape[0], "v")
+    _ints(cu_seqlens, None, q.device, "cu_seqlens")
+    n_seq = cu_seqlens.numel() - 1
+    _need(n_seq >= 0, "cu_seqlens: at least one entry")
+    if out is not None:
+        _packed(out, None, None, "out")
+        _need(out.shape == q.shape and out.device == q.device and out.dtype in _DT and out_dtype in (None, out.dtype),
+              "out: [H, N, d] on the inputs' device")
+    with _On(q.device, stream) as on:
+        on.uses(q, k, v, cu_seqlens, out, workspace)
+        if out is None:
+            out = torch.empty((H, N, d), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            on.hands(out)
+        ws = _ws(workspace, 256, q.device)
+        _check("la_softmax_prefill", lib().la_softmax_prefill(
+            _ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], H, k.shape[0], N, d, _ptr(cu_seqlens), n_seq,
+            _strides(q, k, v, out), d ** -0.5 if scale is None else float(scale), _ptr(out), _DT[out.dtype],
+            _ptr(ws), ws.numel() * ws.element_size(), on.ptr))
+    return out
+
+
+def la_kv4_append(k, v, cache, start, cu_seqlens=None, stream=None):
+    """Quantises tokens into the cache.  k, v: [H_kv, N, d] (views as for
+    la_softmax_prefill); token t of sequence s goes to position start[s] +
+    (t - cu_seqlens[s]); without ``cu_seqlens`` token t is sequence t's only
+    one.  Positions outside the cache are dropped.  start: [B] int32."""
+    c = _cache_c(cache)
+    dev = cache.k_codes.device
+    _packed(k, None, None, "k")
+    _packed(v, k, c.H_kv, "v")
+    _need(k.dtype in _DT and k.device == dev and k.shape[0] == c.H_kv and k.shape[2] == c.d,
+          "k, v: [H_kv, N, d] of the cache's heads and head dim, on its device")
+    _ints(start, c.B, dev, "start")
+    if cu_seqlens is not None:
+        _ints(cu_seqlens, c.B + 1, dev, "cu_seqlens")
+    else:
+        _need(k.shape[1] == c.B, "without cu_seqlens: one token per sequence")
+    with _On(dev, stream) as on:
+        on.uses(k, v, start, cu_seqlens, *cache)
+        _check("la_kv4_append", lib().la_kv4_append(_ptr(k), _ptr(v), _DT[k.dtype], k.shape[1], _strides(k, v),
+                                                    _ptr(cu_seqlens), _ptr(start), ctypes.byref(c), on.ptr))
+
+
+def la_kv4_read(cache, start, n_tokens, cu_seqlens=None, out_dtype=torch.float32, stream=None):
+    """The cache's values at the positions la_kv4_append would write for the
+    same ``start`` and ``cu_seqlens``: (k, v), each [H_kv, n_tokens, d].
+    Positions outside the cache and tokens of no sequence give zeros."""
+    c = _cache_c(cache)
+    dev = cache.k_codes.device
+    _need(out_dtype in _DT and n_tokens >= 0, "out_dtype: f32, bf16 or f16; n_tokens >= 0")
+    _ints(start, c.B, dev, "start")
+    if cu_seqlens is not None:
+        _ints(cu_seqlens, c.B + 1, dev, "cu_seqlens")
+    else:
+        _need(n_tokens == c.B, "without cu_seqlens: one token per sequence")
+    with _On(dev, stream) as on:
+        on.uses(start, cu_seqlens, *cache)
+        k = torch.empty((c.H_kv, n_tokens, c.d), dtype=out_dtype, device=dev)
+        v = torch.empty_like(k)
+        on.hands(k, v)
+        _check("la_kv4_read", lib().la_kv4_read(ctypes.byref(c), n_tokens, _ptr(cu_seqlens), _ptr(start), _ptr(k),
+                                                _ptr(v), _DT[out_dtype], on.ptr))
+    return k, v
+
+
+def la_kv4_decode(q, cache, lens, scale=None, weights_in=None, weights_out=None, out=None, out_dtype=None,
+                  workspace=None, stream=None):
+    """Softmax attention of one query token per sequence over the first
+    lens[b] positions of the cache.  q: [B, H, d] contiguous; lens: [B] int32.
+    ``scale`` defaults to d ** -0.5.  ``weights_out`` [B, H_kv, cap] fp32
+    receives weights_in (zeros if None; may be the same tensor) plus each
+    position's attention weight summed over the head's queries.  Returns
+    ``out`` [B, H, d]; a length of 0 gives zeros."""
+    c = _cache_c(cache)
+    dev = cache.k_codes.device
+    _need(q.dim() == 3 and q.is_contiguous() and q.dtype in _DT and q.device == dev and q.shape[0] == c.B
+          and q.shape[2] == c.d, "q: contiguous [B, H, d] of the cache's sequences and head dim, on its device")
+    H = q.shape[1]
+    _ints(lens, c.B, dev, "lens")
+    for x in (weights_in, weights_out):
+        if x is not None:
+            _need(x.dtype == torch.float32 and tuple(x.shape) == (c.B, c.H_kv, c.cap) and x.device == dev
+                  and x.is_contiguous(), "weights: contiguous [B, H_kv, cap] fp32")
+    if out is not None:
+        _need(out.shape == q.shape and out.is_contiguous() and out.device == dev and out.dtype in _DT
+              and out_dtype in (None, out.dtype), "out: contiguous [B, H, d] on the cache's device")
+    with _On(dev, stream) as on:
+        on.uses(q, lens, weights_in, weights_out, out, workspace, *cache)
+        if out is None:
+            out = torch.empty((c.B, H, c.d), dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
+            on.hands(out)
+        ws = _ws(workspace, la_kv4_decode_workspace_size(c.B, H, c.H_kv, c.cap, c.d, weights_out is not None), dev)
+        _check("la_kv4_decode", lib().la_kv4_decode(
+            _ptr(q), _DT[q.dtype], H, ctypes.byref(c), _ptr(lens), c.d ** -0.5 if scale is None else float(scale),
+            _ptr(weights_in), _ptr(weights_out), _ptr(out), _DT[out.dtype], _ptr(ws),
+            ws.numel() * ws.element_size(), on.ptr))
+    return out
+
+
+def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=None, workspace=None, stream=None):
+    """Cuts every (sequence, head) down to ``keep`` positions: the ``recent``
+    newest and the heaviest of the others (ties to the lower position), moved
+    in their order to the front of ``out``, another cache of at least ``keep``
+    positions (allocated with ``keep`` when None).  weights: [B, H_kv, cap]
+    fp32.  Returns (kept, out_weights, out_lens): the old positions
+    [B, H_kv, keep] int32 (-1 behind them), their weights [B, H_kv, out.cap]
+    and the new lengths [B] int32; with ``out`` None (out, kept, out_weights,
+    out_lens)."""
+    c = _cache_c(cache)
+    dev = cache.k_codes.device
+    keep, recent = int(keep), int(recent)
+    _ints(lens, c.B, dev, "lens")
+    _need(weights.dtype == torch.float32 and tuple(weights.shape) == (c.B, c.H_kv, c.cap) and weights.device == dev
+          and weights.is_contiguous(), "weights: contiguous [B, H_kv, cap] fp32")
+    _need(keep >= 1 and 0 <= recent <= keep, "keep >= 1, 0 <= recent <= keep")
+    if out is not None:
+        _need(_cache_c(out, "out").cap >= keep and out.k_codes.device == dev, "out: keep positions at least, on the cache's device")
+    if out_weights is not None:
+        cap_out = keep if out is None else out.k_codes.shape[2]
+        _need(out_weights.dtype == torch.float32 and tuple(out_weights.shape) == (c.B, c.H_kv, cap_out)
+              and out_weights.device == dev and out_weights.is_contiguous(),
+              "out_weights: contiguous [B, H_kv, out.cap] fp32")
+    with _On(dev, stream) as on:
+        on.uses(weights, lens, out_weights, workspace, *cache, *(out or ()))
+        dst = out
+        if dst is None:
+            dst = KV4Cache.alloc(c.B, c.H_kv, keep, c.d, dev)
+            on.hands(*dst)
+        o = _cache_c(dst, "out")
+        if out_weights is None:
+            out_weights = torch.zeros((c.B, c.H_kv, o.cap), dtype=torch.float32, device=dev)
+            on.hands(out_weights)
+        kept = torch.empty((c.B, c.H_kv, keep), dtype=torch.int32, device=dev)
+        out_lens = torch.empty(c.B, dtype=torch.int32, device=dev)
+        on.hands(kept, out_lens)
+        ws = _ws(workspace, la_kv4_evict_workspace_size(c.B, c.H_kv, c.cap, keep), dev)
+        _check("la_kv4_evict", lib().la_kv4_evict(ctypes.byref(c), _ptr(weights), _ptr(lens), keep, recent,
+                                                  ctypes.byref(o), _ptr(out_weights), _ptr(kept), _ptr(out_lens),
+                                                  _ptr(ws), ws.numel() * ws.element_size(), on.ptr))
+    return (dst, kept, out_weights, out_lens) if out is None else (kept, out_weights, out_lens)

@@ -1,0 +1,134 @@
+// kv4_append.cuh — writing tokens into the 4-bit cache and reading them back.
+//
+// Eight threads per row (a token of one head, keys or values): thread r holds
+// channels 4 r .. 4 r + 3 of every group, which are the row's chunk r, so its
+// codes are one store of D / 16 bytes, and a group's minimum, maximum and
+// largest magnitude take three shuffles.  Each input is read once and each
+// cache byte written once; bound by memory.
+#pragma once
+#include "kv4_format.cuh"
+#include "packed.cuh"
+#include "softmax_simt.cuh"
+
+namespace la {
+
+struct Kv4CacheDev {
+    uint8_t *k_codes;
+    uint32_t *k_par;
+    uint8_t *v_codes;
+    uint32_t *v_par;
+    int B, Hkv, cap;
+};
+
+struct Kv4AppendParams {
+    const void *k, *v;
+    long k_hs, k_ts, v_hs, v_ts;
+    const int32_t *cu;      // or null: token t is sequence t's only one
+    const int32_t *start;
+    Kv4CacheDev c;
+    int N;
+    void *k_out, *v_out;    // kv4_read
+};
+
+constexpr int kAppendThreads = 256;
+
+// The cache row of token t, or -1 if it has none.
+__device__ __forceinline__ long kv4_row(const Kv4AppendParams &p, int t, int head) {
+    int s = t, i = 0;
+    if (p.cu) {
+        s = seq_of_token(p.cu, p.c.B, p.N, t);
+        const int b = seq_start(p.cu, s, p.N);
+        i = t - b;
+        if (i < 0 || t >= seq_start(p.cu, s + 1, p.N)) return -1;   // of no sequence
+    }
+    const long pos = (long)p.start[s] + i;
+    if (pos < 0 || pos >= p.c.cap) return -1;
+    return ((long)s * p.c.Hkv + head) * p.c.cap + pos;
+}
+
+template <int D> struct Kv4Chunk;   // a chunk: one 16-bit field per group
+template <> struct Kv4Chunk<32> { using type = uint16_t; };
+template <> struct Kv4Chunk<64> { using type = uint32_t; };
+template <> struct Kv4Chunk<128> { using type = uint64_t; };
+
+template <typename InT, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendParams p) {
+    constexpr int G = D / kKv4Group;
+    using Chunk = typename Kv4Chunk<D>::type;
+    const int r = threadIdx.x & 7, head = blockIdx.y;
+    const bool keys = blockIdx.z == 0;
+    const InT *x = keys ? (const InT *)p.k + head * p.k_hs : (const InT *)p.v + head * p.v_hs;
+    const long ts = keys ? p.k_ts : p.v_ts;
+    uint8_t *codes = keys ? p.c.k_codes : p.c.v_codes;
+    uint32_t *par = keys ? p.c.k_par : p.c.v_par;
+    const int step = gridDim.x * (kAppendThreads / 8);
+    // a warp's four rows go round together, so that its shuffles are whole
+    for (int t0 = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 5) * 4; t0 < p.N; t0 += step) {
+        const int t = t0 + ((threadIdx.x & 31) >> 3);
+        const long row = t < p.N ? kv4_row(p, t, head) : -1;
+        float v[G][4];
+        uint32_t word = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= 0) f = load4<InT>(x + (long)t * ts + g * kKv4Group + r * 4);
+            v[g][0] = f.x; v[g][1] = f.y; v[g][2] = f.z; v[g][3] = f.w;
+            float lo = fminf(fminf(f.x, f.y), fminf(f.z, f.w)), hi = fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w));
+            // magnitudes as bits: a NaN or an infinity is the largest
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(v[g][i]) & 0x7fffffffu);
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) {
+                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+                a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+            }
+            // thread g of the eight forms group g's word (its float64 divisions once per group)
+            if (r == g) word = kv4_word(lo, hi, a);
+        }
+        Chunk chunk = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint32_t w = __shfl_sync(0xffffffffu, word, g, 8);
+            const float sc = kv4_scale(w), of = kv4_offset(w), inv = 1.f / sc;
+            uint32_t f = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f |= kv4_code(v[g][i], sc, inv, of) << (4 * i);
+            chunk |= (Chunk)((Chunk)f << (16 * g));
+        }
+        if (row >= 0) {
+            reinterpret_cast<Chunk *>(codes)[row * 8 + r] = chunk;
+            if (r < G) par[row * G + r] = word;
+        }
+    }
+}
+
+template <typename OutT, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(Kv4AppendParams p) {
+    constexpr int G = D / kKv4Group;
+    using Chunk = typename Kv4Chunk<D>::type;
+    pdl_wait();
+    const int r = threadIdx.x & 7, head = blockIdx.y;
+    const bool keys = blockIdx.z == 0;
+    const uint8_t *codes = keys ? p.c.k_codes : p.c.v_codes;
+    const uint32_t *par = keys ? p.c.k_par : p.c.v_par;
+    OutT *out = keys ? (OutT *)p.k_out : (OutT *)p.v_out;
+    const int step = gridDim.x * (kAppendThreads / 8);
+    for (int t = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 3); t < p.N; t += step) {
+        const long row = kv4_row(p, t, head);
+        Chunk chunk = 0;
+        if (row >= 0) chunk = reinterpret_cast<const Chunk *>(codes)[row * 8 + r];
+        OutT *dst = out + ((long)head * p.N + t) * D + r * 4;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint32_t w = row >= 0 ? par[row * G + g] : 0u;
+            const float sc = kv4_scale(w), of = kv4_offset(w);
+            const uint32_t f = (uint32_t)(chunk >> (16 * g)) & 0xffffu;
+            store4<OutT>(dst + g * kKv4Group, sc * ((float)(f & 15) + of), sc * ((float)((f >> 4) & 15) + of),
+                         sc * ((float)((f >> 8) & 15) + of), sc * ((float)(f >> 12) + of));
+        }
+    }
+}
+
+}  // namespace la

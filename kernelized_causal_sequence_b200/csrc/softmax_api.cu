@@ -1,0 +1,300 @@
+// softmax_api.cu — the softmax operators of include/linattn.h: argument
+// checks, workspace layout and dispatch.  Everything is checked on the host
+// before anything is launched.
+#include <cmath>
+#include <cstring>
+
+#include "errors.h"
+#include "kv4_append.cuh"
+#include "kv4_decode.cuh"
+#include "kv4_evict.cuh"
+#include "launch.h"
+#include "linattn.h"
+#include "plan.h"
+#include "softmax_simt.cuh"
+
+using namespace la;
+
+namespace {
+
+constexpr size_t kWsAlign = 256;
+constexpr int kMaxTokens = 1 << 30;   // N and n_seq: tile numbers and row indexes stay in 32 bits
+inline size_t ws_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
+inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool dt_ok(la_dtype t) { return t == LA_F32 || t == LA_BF16 || t == LA_F16; }
+inline bool d_ok(int d) { return d == 32 || d == 64 || d == 128; }
+inline int esize(la_dtype t) { return t == LA_F32 ? 4 : 2; }
+inline bool ws_ok(const void *ws, size_t have, size_t need) {
+    return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) == 0);
+}
+
+la_status check_types(la_dtype in, la_dtype out, int d) {
+    if (!dt_ok(in) || !dt_ok(out) || d <= 0) return LA_ERR_INVALID_ARG;
+    if (!d_ok(d) || !(out == in || out == LA_F32)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// Query heads over key/value heads.
+la_status check_heads(int H, int H_kv) {
+    if (H < 0 || H_kv < 0 || (H_kv == 0) != (H == 0)) return LA_ERR_INVALID_ARG;
+    if (H == 0) return LA_OK;
+    if (H % H_kv) return LA_ERR_INVALID_ARG;
+    return H > 65535 ? LA_ERR_UNSUPPORTED : LA_OK;   // heads run along grid y
+}
+
+// One tensor's (head, token) strides: given or contiguous.  A stride of an
+// extent of at most 1 is never used and is replaced by a valid one.
+bool set_strides(const int64_t *s, int heads, int N, int d, int es, long *hs, long *ts) {
+    *ts = d;
+    *hs = (long)N * d;
+    if (!s) return true;
+    const int per16 = 16 / es;
+    if (N > 1) {
+        if (s[1] < d || s[1] % per16 || s[1] >= (1L << 39) / es) return false;
+        *ts = s[1];
+        *hs = s[1] * N;
+    }
+    if (heads > 1) {
+        if (s[0] < d || s[0] % per16 || s[0] >= (1L << 39) / es) return false;
+        *hs = s[0];
+    }
+    return true;
+}
+
+// Bytes from a tensor's first to behind its last element.
+inline size_t span(int heads, int N, int d, long hs, long ts, int es) {
+    return ((size_t)(heads - 1) * hs + (size_t)(N - 1) * ts + d) * es;
+}
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+la_status check_cache(const la_kv4_cache *c) {
+    if (!c || c->B < 0 || c->H_kv < 0 || c->cap < 0 || c->d <= 0) return LA_ERR_INVALID_ARG;
+    if (!d_ok(c->d)) return LA_ERR_UNSUPPORTED;
+    if (c->H_kv > 65535 || c->B > 65535 || c->cap > kMaxTokens) return LA_ERR_UNSUPPORTED;
+    if ((long)c->B * c->H_kv * c->cap == 0) return LA_OK;
+    if (!c->k_codes || !c->k_par || !c->v_codes || !c->v_par || !al16(c->k_codes) || !al16(c->k_par) ||
+        !al16(c->v_codes) || !al16(c->v_par))
+        return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+Kv4CacheDev dev_cache(const la_kv4_cache *c) {
+    return Kv4CacheDev{c->k_codes, c->k_par, c->v_codes, c->v_par, c->B, c->H_kv, c->cap};
+}
+inline size_t code_bytes(const la_kv4_cache *c) { return (size_t)c->B * c->H_kv * c->cap * (c->d / 2); }
+inline size_t par_bytes(const la_kv4_cache *c) { return (size_t)c->B * c->H_kv * c->cap * (c->d / 8); }
+
+// Grid x of a kernel that strides over `items` in blocks of `per`: enough
+// blocks, over `others` grid rows, for about eight waves of one block per SM.
+inline unsigned stride_grid(long items, int per, long others) {
+    const long need = (items + per - 1) / per, most = (8L * kNumSMs + others - 1) / others;
+    return (unsigned)(need < most ? need : most);
+}
+
+#define LA_BY_D(d, CALL)                    \
+    switch (d) {                            \
+        case 32: { constexpr int D = 32; CALL; }   \
+        case 64: { constexpr int D = 64; CALL; }   \
+        case 128: { constexpr int D = 128; CALL; } \
+        default: return LA_ERR_UNSUPPORTED; \
+    }
+#define LA_BY_TYPES(in, out, CALL)                                                          \
+    if (in == LA_F32) { using InT = float; using OutT = float; CALL; }                      \
+    if (in == LA_BF16 && out == LA_BF16) { using InT = bf16; using OutT = bf16; CALL; }     \
+    if (in == LA_BF16) { using InT = bf16; using OutT = float; CALL; }                      \
+    if (out == LA_F16) { using InT = f16; using OutT = f16; CALL; }                         \
+    { using InT = f16; using OutT = float; CALL; }
+
+template <typename InT, typename OutT>
+la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
+    LA_BY_D(d, return launch_kernel(softmax_simt_kernel<InT, OutT, D>,
+                                    dim3((unsigned)seq_tiles(p.N, p.n_seq, kSsTile), (unsigned)p.H), dim3(kSsThreads),
+                                    softmax_simt_smem<D>(), st, false, "softmax prefill launch", p))
+}
+template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
+    const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
+    LA_BY_D(d, return launch_kernel(kv4_append_kernel<InT, D>, grid, dim3(kAppendThreads), 0, st, false,
+                                    "kv4 append launch", p))
+}
+template <typename OutT> la_status run_read(const Kv4AppendParams &p, int d, cudaStream_t st) {
+    const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
+    LA_BY_D(d, return launch_kernel(kv4_read_kernel<OutT, D>, grid, dim3(kAppendThreads), 0, st, true,
+                                    "kv4 read launch", p))
+}
+template <typename InT, typename OutT> la_status run_decode(const Kv4DecodeParams &p, int d, cudaStream_t st) {
+    LA_BY_D(d, return launch_kernel(kv4_decode_kernel<InT, OutT, D>, dim3((unsigned)p.H, (unsigned)p.c.B),
+                                    dim3(kDecWarps * 32), 0, st, true, "kv4 decode launch", p))
+}
+
+struct DecodeWs { size_t scores, lse, bytes; };
+DecodeWs decode_ws(int B, int H, int cap, int with_weights) {
+    DecodeWs w{0, 0, 0};
+    if (!with_weights) return w;
+    w.lse = ws_up((size_t)B * H * cap * sizeof(float));
+    w.bytes = ws_up(w.lse + (size_t)B * H * sizeof(float));
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la_softmax_prefill_workspace_size(int H, int H_kv, int N, int d, int n_seq) {
+    if (H <= 0 || H_kv <= 0 || H % H_kv || N <= 0 || n_seq <= 0 || !d_ok(d)) return 0;
+    return kWsAlign;
+}
+
+la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dtype in_dtype, int H, int H_kv,
+                             int N, int d, const int32_t *cu_seqlens, int n_seq, const int64_t *strides,
+                             float scale, void *out, la_dtype out_dtype, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    la_status s = check_types(in_dtype, out_dtype, d);
+    if (s != LA_OK || (s = check_heads(H, H_kv)) != LA_OK) return s;
+    if (N < 0 || n_seq < 0 || !(std::isfinite(scale) && scale > 0.f)) return LA_ERR_INVALID_ARG;
+    if (N > kMaxTokens || n_seq > kMaxTokens) return LA_ERR_UNSUPPORTED;
+    SoftmaxParams p;
+    const int ie = esize(in_dtype), oe = esize(out_dtype);
+    if (!set_strides(strides, H, N, d, ie, &p.q_hs, &p.q_ts) ||
+        !set_strides(strides ? strides + 2 : nullptr, H_kv, N, d, ie, &p.k_hs, &p.k_ts) ||
+        !set_strides(strides ? strides + 4 : nullptr, H_kv, N, d, ie, &p.v_hs, &p.v_ts) ||
+        !set_strides(strides ? strides + 6 : nullptr, H, N, d, oe, &p.o_hs, &p.o_ts))
+        return LA_ERR_INVALID_ARG;
+    if (H == 0 || N == 0 || n_seq == 0) return LA_OK;
+    if (!q || !k || !v || !out || !cu_seqlens || !al16(q) || !al16(k) || !al16(v) || !al16(out) || !al4(cu_seqlens))
+        return LA_ERR_INVALID_ARG;
+    const size_t os = span(H, N, d, p.o_hs, p.o_ts, oe);
+    if (overlap(out, os, q, span(H, N, d, p.q_hs, p.q_ts, ie)) ||
+        overlap(out, os, k, span(H_kv, N, d, p.k_hs, p.k_ts, ie)) ||
+        overlap(out, os, v, span(H_kv, N, d, p.v_hs, p.v_ts, ie)) ||
+        overlap(out, os, cu_seqlens, sizeof(int32_t) * ((size_t)n_seq + 1)))
+        return LA_ERR_INVALID_ARG;
+    if (!ws_ok(workspace, workspace_bytes, kWsAlign)) return LA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 2 * sizeof(int), st))) != LA_OK) return s;
+    p.q = q; p.k = k; p.v = v; p.out = out; p.cu = cu_seqlens;
+    p.H = H; p.group = H / H_kv; p.N = N; p.n_seq = n_seq;
+    p.scale_log2 = scale * kLog2e;
+    LA_BY_TYPES(in_dtype, out_dtype, return (run_softmax_simt<InT, OutT>(p, d, st)))
+}
+
+la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, const int64_t *strides,
+                        const int32_t *cu_seqlens, const int32_t *start, const la_kv4_cache *cache, void *stream) {
+    la_status s = check_cache(cache);
+    if (s != LA_OK) return s;
+    if (!dt_ok(in_dtype) || N < 0 || (!cu_seqlens && N != cache->B)) return LA_ERR_INVALID_ARG;
+    if (N > kMaxTokens) return LA_ERR_UNSUPPORTED;
+    Kv4AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int es = esize(in_dtype);
+    if (!set_strides(strides, cache->H_kv, N, cache->d, es, &p.k_hs, &p.k_ts) ||
+        !set_strides(strides ? strides + 2 : nullptr, cache->H_kv, N, cache->d, es, &p.v_hs, &p.v_ts))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0 || cache->B == 0 || cache->H_kv == 0 || cache->cap == 0) return LA_OK;
+    if (!k || !v || !start || !al16(k) || !al16(v) || !al4(start) || !al4(cu_seqlens)) return LA_ERR_INVALID_ARG;
+    p.k = k; p.v = v; p.cu = cu_seqlens; p.start = start; p.c = dev_cache(cache); p.N = N;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (in_dtype == LA_F32) return run_append<float>(p, cache->d, st);
+    if (in_dtype == LA_BF16) return run_append<bf16>(p, cache->d, st);
+    return run_append<f16>(p, cache->d, st);
+}
+
+la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlens, const int32_t *start,
+                      void *k_out, void *v_out, la_dtype out_dtype, void *stream) {
+    la_status s = check_cache(cache);
+    if (s != LA_OK) return s;
+    if (!dt_ok(out_dtype) || N < 0 || (!cu_seqlens && N != cache->B)) return LA_ERR_INVALID_ARG;
+    if (N > kMaxTokens) return LA_ERR_UNSUPPORTED;
+    if (N == 0 || cache->B == 0 || cache->H_kv == 0) return LA_OK;
+    if (!k_out || !v_out || !start || !al16(k_out) || !al16(v_out) || !al4(start) || !al4(cu_seqlens))
+        return LA_ERR_INVALID_ARG;
+    Kv4AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.cu = cu_seqlens; p.start = start; p.c = dev_cache(cache); p.N = N; p.k_out = k_out; p.v_out = v_out;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (out_dtype == LA_F32) return run_read<float>(p, cache->d, st);
+    if (out_dtype == LA_BF16) return run_read<bf16>(p, cache->d, st);
+    return run_read<f16>(p, cache->d, st);
+}
+
+size_t la_kv4_decode_workspace_size(int B, int H, int H_kv, int cap, int d, int with_weights) {
+    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv || cap <= 0 || cap > kMaxTokens || !d_ok(d)) return 0;
+    return decode_ws(B, H, cap, with_weights).bytes;
+}
+
+la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_cache *cache, const int32_t *lens,
+                        float scale, const float *weights_in, float *weights_out, void *out, la_dtype out_dtype,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    la_status s = check_cache(cache);
+    if (s != LA_OK || (s = check_types(in_dtype, out_dtype, cache->d)) != LA_OK ||
+        (s = check_heads(H, cache->H_kv)) != LA_OK)
+        return s;
+    if (!(std::isfinite(scale) && scale > 0.f) || (weights_in && !weights_out)) return LA_ERR_INVALID_ARG;
+    if (H == 0 || cache->B == 0) return LA_OK;
+    if (!q || !lens || !out || !al16(q) || !al16(out) || !al4(lens) || !al16(weights_in) || !al16(weights_out))
+        return LA_ERR_INVALID_ARG;
+    const size_t wb = (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float);
+    if (weights_in != weights_out && overlap(weights_in, wb, weights_out, wb)) return LA_ERR_INVALID_ARG;
+    const DecodeWs wl = decode_ws(cache->B, H, cache->cap, weights_out != nullptr);
+    if (!ws_ok(workspace, workspace_bytes, wl.bytes)) return LA_ERR_INVALID_ARG;
+    Kv4DecodeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.q = q; p.c = dev_cache(cache); p.lens = lens; p.weights_in = weights_in; p.weights_out = weights_out;
+    p.out = out; p.H = H; p.group = H / cache->H_kv; p.scale_log2 = scale * kLog2e;
+    p.scores = (float *)((char *)workspace + wl.scores);
+    p.lse = (float *)((char *)workspace + wl.lse);
+    cudaStream_t st = (cudaStream_t)stream;
+    LA_BY_TYPES(in_dtype, out_dtype, s = (run_decode<InT, OutT>(p, cache->d, st)); goto decoded)
+decoded:
+    if (s != LA_OK || !weights_out || cache->cap == 0) return s;
+    return launch_kernel(kv4_weights_kernel,
+                         dim3(stride_grid(cache->cap, 256, (long)cache->H_kv * cache->B), (unsigned)cache->H_kv,
+                              (unsigned)cache->B),
+                         dim3(256), 0, st, true, "kv4 weights launch", p);
+}
+
+size_t la_kv4_evict_workspace_size(int B, int H_kv, int cap, int keep) {
+    if (B <= 0 || H_kv <= 0 || cap <= 0 || cap > kMaxTokens || keep < 1) return 0;
+    return ws_up((size_t)B * H_kv * keep * sizeof(int32_t));
+}
+
+la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const int32_t *lens, int keep, int recent,
+                       const la_kv4_cache *out, float *out_weights, int32_t *kept, int32_t *out_lens,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+    la_status s = check_cache(cache);
+    if (s != LA_OK || (s = check_cache(out)) != LA_OK) return s;
+    if (out->B != cache->B || out->H_kv != cache->H_kv || out->d != cache->d || keep < 1 || recent < 0 ||
+        recent > keep || out->cap < keep)
+        return LA_ERR_INVALID_ARG;
+    if (cache->B == 0 || cache->H_kv == 0) return LA_OK;
+    if (!lens || !al4(lens) || !al4(kept) || !al4(out_lens) || !al16(out_weights)) return LA_ERR_INVALID_ARG;
+    if (cache->cap > 0 && (!weights || !al16(weights))) return LA_ERR_INVALID_ARG;
+    const void *src[4] = {cache->k_codes, cache->v_codes, cache->k_par, cache->v_par};
+    const void *dst[4] = {out->k_codes, out->v_codes, out->k_par, out->v_par};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
+            if (overlap(src[i], i < 2 ? code_bytes(cache) : par_bytes(cache), dst[j],
+                        j < 2 ? code_bytes(out) : par_bytes(out)))
+                return LA_ERR_INVALID_ARG;
+    if (overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), out_weights,
+                (size_t)out->B * out->H_kv * out->cap * sizeof(float)))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = ws_up((size_t)cache->B * cache->H_kv * keep * sizeof(int32_t));
+    if (!ws_ok(workspace, workspace_bytes, need)) return LA_ERR_INVALID_ARG;
+    Kv4EvictParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.c = dev_cache(cache); p.o = dev_cache(out); p.weights = weights; p.lens = lens; p.keep = keep;
+    p.recent = recent; p.out_weights = out_weights; p.kept = kept; p.out_lens = out_lens;
+    p.list = (int32_t *)workspace;
+    cudaStream_t st = (cudaStream_t)stream;
+    s = launch_kernel(kv4_select_kernel, dim3((unsigned)cache->H_kv, (unsigned)cache->B), dim3(kEvictThreads), 0, st,
+                      false, "kv4 select launch", p);
+    if (s != LA_OK || cache->cap == 0) return s;
+    const dim3 grid(stride_grid(keep < cache->cap ? keep : cache->cap, 32, (long)cache->H_kv * cache->B),
+                    (unsigned)cache->H_kv, (unsigned)cache->B);
+    LA_BY_D(cache->d, return launch_kernel(kv4_gather_kernel<D>, grid, dim3(256), 0, st, true, "kv4 gather launch", p))
+}
+
+}  // extern "C"

@@ -1,0 +1,150 @@
+"""Host-side checks of the softmax operators: bad arguments are refused before
+anything is launched (these calls never reach the GPU, so they run anywhere)."""
+import ctypes
+
+import pytest
+import torch
+
+import kernelized_causal_sequence_b200 as la
+
+INVALID, UNSUPPORTED = la.LA_ERR_INVALID_ARG, la.LA_ERR_UNSUPPORTED
+BASE = 1 << 40      # dummy addresses, never dereferenced, 4 GiB apart
+
+
+def P(i, off=0):
+    return ctypes.c_void_p(BASE + (i << 32) + off)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from kernelized_causal_sequence_b200 import build
+    build.build()
+    return la.lib()
+
+
+@pytest.fixture(autouse=True)
+def no_kernel_launched(L):
+    before = L.la_launch_count()
+    yield
+    assert L.la_launch_count() == before, "a host-side check let a kernel launch"
+
+
+def prefill(L, **kw):
+    a = dict(q=P(1), k=P(2), v=P(3), dt=la.LA_BF16, H=8, Hkv=2, N=1000, d=128, cu=P(4), n_seq=3, strides=None,
+             scale=0.1, out=P(5), odt=la.LA_BF16, ws=P(6), nws=256)
+    a.update(kw)
+    if a["strides"] is not None:
+        a["strides"] = (ctypes.c_int64 * 8)(*a["strides"])
+    return L.la_softmax_prefill(a["q"], a["k"], a["v"], a["dt"], a["H"], a["Hkv"], a["N"], a["d"], a["cu"], a["n_seq"],
+                                a["strides"], a["scale"], a["out"], a["odt"], a["ws"], a["nws"], None)
+
+
+C = [1000 * 128, 128]
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(out=None), INVALID),
+    (dict(cu=None), INVALID), (dict(cu=P(4, 2)), INVALID), (dict(q=P(1, 8)), INVALID), (dict(out=P(5, 8)), INVALID),
+    (dict(dt=7), INVALID), (dict(odt=-1), INVALID), (dict(odt=la.LA_F16), UNSUPPORTED), (dict(dt=la.LA_F32), UNSUPPORTED),
+    (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(d=0), INVALID), (dict(H=-1), INVALID),
+    (dict(H=7), INVALID), (dict(Hkv=0), INVALID), (dict(H=0), INVALID), (dict(H=70000, Hkv=70000), UNSUPPORTED),
+    (dict(N=-1), INVALID), (dict(N=(1 << 30) + 1), UNSUPPORTED), (dict(n_seq=-1), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(ws=None), INVALID), (dict(nws=255), INVALID), (dict(ws=P(6, 64)), INVALID),
+    (dict(out=P(1)), INVALID), (dict(out=P(1, 1000 * 128 * 16 - 16)), INVALID), (dict(out=P(2)), INVALID),
+    (dict(out=P(3)), INVALID), (dict(strides=C + [0, 128] + C + C), INVALID), (dict(strides=C + C + C + [1000 * 128, 64]), INVALID),
+    (dict(strides=[1000 * 132, 132] + C + C + C), INVALID), (dict(strides=C + C + [1 << 40, 128] + C), INVALID),
+    (dict(strides=[-1000 * 128, 128] + C + C + C), INVALID),
+])
+def test_prefill_refusals(L, kw, want):
+    assert prefill(L, **kw) == want
+
+
+def test_prefill_nothing_to_do(L):
+    for kw in (dict(N=0), dict(n_seq=0), dict(H=0, Hkv=0)):
+        assert prefill(L, **kw) == la.LA_OK
+    assert la.la_softmax_prefill_workspace_size(8, 2, 100, 128, 1) >= 8
+    assert la.la_softmax_prefill_workspace_size(8, 3, 100, 128, 1) == 0
+    assert la.la_softmax_prefill_workspace_size(8, 2, 100, 80, 1) == 0
+
+
+def cache(i=10, **kw):
+    a = dict(k_codes=P(i), k_par=P(i + 1), v_codes=P(i + 2), v_par=P(i + 3), B=3, H_kv=2, cap=100, d=64)
+    a.update(kw)
+    return la._Kv4CacheC(*(x.value if isinstance(x, ctypes.c_void_p) else x for x in a.values()))
+
+
+BAD_CACHES = [(dict(k_codes=None), INVALID), (dict(k_par=P(11, 4)), INVALID), (dict(v_codes=P(12, 8)), INVALID),
+              (dict(v_par=None), INVALID), (dict(d=48), UNSUPPORTED), (dict(d=0), INVALID), (dict(B=-1), INVALID),
+              (dict(cap=-1), INVALID), (dict(H_kv=-1), INVALID), (dict(cap=(1 << 30) + 1), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,want", BAD_CACHES)
+def test_bad_caches(L, kw, want):
+    c = ctypes.byref(cache(**kw))
+    good = ctypes.byref(cache(20))
+    assert L.la_kv4_append(P(1), P(2), 1, 3, None, None, P(3), c, None) == want
+    assert L.la_kv4_read(c, 3, None, P(3), P(1), P(2), 1, None) == want
+    assert L.la_kv4_decode(P(1), 1, 4, c, P(2), 0.1, None, None, P(3), 1, P(4), 1 << 30, None) == want
+    assert L.la_kv4_evict(c, P(1), P(2), 10, 0, good, None, None, None, P(3), 1 << 30, None) == want
+    assert L.la_kv4_evict(good, P(1), P(2), 10, 0, c, None, None, None, P(3), 1 << 30, None) == want
+
+
+def test_append_read_refusals(L):
+    c = ctypes.byref(cache())
+    app = lambda k=P(1), v=P(2), dt=1, N=50, st=None, cu=P(3), start=P(4): L.la_kv4_append(
+        k, v, dt, N, None if st is None else (ctypes.c_int64 * 4)(*st), cu, start, c, None)
+    assert app(k=None) == app(v=None) == app(start=None) == app(k=P(1, 8)) == app(start=P(4, 1)) == INVALID
+    assert app(cu=P(3, 2)) == app(dt=5) == app(N=-1) == app(cu=None) == INVALID
+    assert app(st=[50 * 64, 63, 50 * 64, 64]) == app(st=[50 * 64, 64, 50 * 64 + 4, 64]) == INVALID
+    assert app(N=(1 << 30) + 1) == UNSUPPORTED
+    assert app(N=0) == la.LA_OK
+    rd = lambda N=50, cu=P(3), start=P(4), k=P(1), v=P(2), dt=1: L.la_kv4_read(c, N, cu, start, k, v, dt, None)
+    assert rd(N=-1) == rd(cu=None) == rd(start=None) == rd(k=None) == rd(v=P(2, 4)) == rd(dt=9) == INVALID
+    assert rd(N=(1 << 30) + 1) == UNSUPPORTED
+    assert rd(N=0) == la.LA_OK
+
+
+def test_decode_refusals(L):
+    c = ctypes.byref(cache())
+    need = la.la_kv4_decode_workspace_size(3, 4, 2, 100, 64, True)
+    assert need > 0
+
+    def dec(q=P(1), dt=1, H=4, lens=P(2), scale=0.1, wi=P(5), wo=P(6), out=P(3), odt=1, ws=P(4), nws=need):
+        return L.la_kv4_decode(q, dt, H, c, lens, scale, wi, wo, out, odt, ws, nws, None)
+    assert dec(q=None) == dec(lens=None) == dec(out=None) == dec(q=P(1, 4)) == dec(lens=P(2, 2)) == INVALID
+    assert dec(dt=9) == dec(H=3) == dec(H=-2) == dec(scale=0.0) == dec(scale=float("nan")) == INVALID
+    assert dec(wo=None) == dec(wi=P(5, 4)) == dec(wo=P(6, 8)) == dec(wi=P(6, 16)) == INVALID
+    assert dec(ws=None) == dec(nws=need - 1) == dec(ws=P(4, 16)) == INVALID
+    assert dec(odt=2) == dec(H=70000) == UNSUPPORTED
+    assert la.la_kv4_decode_workspace_size(3, 5, 2, 100, 64) == 0
+
+
+def test_evict_refusals(L):
+    need = la.la_kv4_evict_workspace_size(3, 2, 100, 10)
+    assert need > 0
+
+    def ev(c=None, o=None, w=P(1), lens=P(2), keep=10, recent=0, ow=P(5), kept=P(6), ol=P(7), ws=P(3), nws=need):
+        return L.la_kv4_evict(ctypes.byref(c or cache()), w, lens, keep, recent, ctypes.byref(o or cache(20, cap=12)),
+                              ow, kept, ol, ws, nws, None)
+    assert ev(w=None) == ev(lens=None) == ev(w=P(1, 4)) == ev(lens=P(2, 1)) == ev(kept=P(6, 2)) == INVALID
+    assert ev(ol=P(7, 2)) == ev(ow=P(5, 4)) == ev(ow=P(1)) == INVALID
+    assert ev(keep=0) == ev(recent=-1) == ev(recent=11) == ev(keep=13) == INVALID
+    assert ev(o=cache(20, B=2)) == ev(o=cache(20, H_kv=1)) == ev(o=cache(20, d=32)) == INVALID
+    assert ev(o=cache(10)) == ev(o=cache(20, v_codes=P(10))) == ev(o=cache(20, k_par=P(13))) == INVALID
+    assert ev(ws=None) == ev(nws=need - 1) == ev(ws=P(3, 32)) == INVALID
+
+
+def test_python_checks():
+    f = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
+    i = lambda n: torch.zeros(n, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        la.la_softmax_prefill(f(4, 10, 64), f(2, 10, 64), f(2, 10, 64), i(3))     # not on CUDA
+    with pytest.raises(ValueError):
+        la.la_softmax_prefill(f(10, 64), f(2, 10, 64), f(2, 10, 64), i(3))
+    c = la.KV4Cache.alloc(2, 1, 8, 64, "cpu")
+    assert [tuple(x.shape) for x in c] == [(2, 1, 8, 32), (2, 1, 8, 2)] * 2
+    for call in (lambda: la.la_kv4_append(f(1, 2, 64), f(1, 2, 64), c, i(2)), lambda: la.la_kv4_read(c, i(2), 2),
+                 lambda: la.la_kv4_decode(f(2, 4, 64), c, i(2)), lambda: la.la_kv4_evict(c, f(2, 1, 8), i(2), 4)):
+        with pytest.raises(ValueError):
+            call()
