@@ -349,7 +349,7 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  * Keys and values behind a query, or of another sequence, do not reach it,
  * not even as NaN or infinity.  Sums and the running maximum are fp32; with
  * 16-bit inputs at d 64 or 128 (the tensor-core kernel) the unnormalised
- * weights, which lie in [0, 1], are rounded once to the input type for the
+ * weights, which lie in [0, 256], are rounded once to the input type for the
  * product with v.
  * The workspace (la_softmax_prefill_workspace_size bytes, 256-byte aligned)
  * starts with the status word that la_workspace_status reads.

@@ -15,6 +15,7 @@
 #include "plan.h"
 #include "scan.h"
 #include "simt_kernels.cuh"
+#include "softmax_tc.h"
 #include "tc_launch.h"
 
 using namespace la;
@@ -72,6 +73,7 @@ template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
 
 namespace la {
 std::atomic<uint64_t> g_launches{0};
+unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 thread_local char g_last_error[256] = "";

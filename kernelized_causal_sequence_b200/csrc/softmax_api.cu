@@ -12,6 +12,7 @@
 #include "linattn.h"
 #include "plan.h"
 #include "softmax_simt.cuh"
+#include "softmax_tc.h"
 
 using namespace la;
 
@@ -177,6 +178,8 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
     p.q = q; p.k = k; p.v = v; p.out = out; p.cu = cu_seqlens;
     p.H = H; p.group = H / H_kv; p.N = N; p.n_seq = n_seq;
     p.scale_log2 = scale * kLog2e;
+    if (softmax_tc_supported(in_dtype, d))
+        return softmax_tc(p, in_dtype, out_dtype, d, (int *)workspace, wait_limit_ns(), st);
     LA_BY_TYPES(in_dtype, out_dtype, return (run_softmax_simt<InT, OutT>(p, d, st)))
 }
 

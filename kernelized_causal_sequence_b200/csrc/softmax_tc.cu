@@ -1,0 +1,83 @@
+// softmax_tc.cu — tensor maps and launch of the tensor-core softmax prefill.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "launch.h"
+#include "softmax_tc.cuh"
+#include "softmax_tc.h"
+
+namespace la {
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// [heads][N][d] with strides, boxes of 64 channels x 128 rows, 128-byte
+// swizzle, zeros past N
+bool map16(CUtensorMap *m, const void *base, la_dtype dt, int heads, int N, int d, long hs, long ts) {
+    auto enc = encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)ts * 2, (cuuint64_t)hs * 2};
+    cuuint32_t box[3] = {64, 128, 1};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, dt == LA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename InT, typename OutT, int D, bool PAIR>
+la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
+    CUtensorMap mq, mk, mv;
+    const int Hk = sp.H / sp.group;
+    if (!map16(&mq, sp.q, dt, sp.H, sp.N, D, sp.q_hs, sp.q_ts) || !map16(&mk, sp.k, dt, Hk, sp.N, D, sp.k_hs, sp.k_ts) ||
+        !map16(&mv, sp.v, dt, Hk, sp.N, D, sp.v_hs, sp.v_ts))
+        return cuda_fail_msg("cuTensorMapEncodeTiled", "tensor map encoding failed");
+    stc::Params p;
+    p.out = sp.out; p.cu = sp.cu; p.o_hs = sp.o_hs; p.o_ts = sp.o_ts;
+    p.H = sp.H; p.group = sp.group; p.N = sp.N; p.n_seq = sp.n_seq;
+    p.tiles = seq_tiles(sp.N, sp.n_seq, PAIR ? 128 : 256);
+    p.scale_log2 = sp.scale_log2; p.status = status; p.wait_ns = wait_ns;
+    const long grid = (long)p.tiles * (PAIR ? sp.H / 2 : sp.H);
+    if (grid > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
+    return launch_kernel(stc::softmax_tc_kernel<InT, OutT, D, PAIR>, dim3((unsigned)grid), dim3(stc::kThreads),
+                         stc::Cfg<D>::SMEM, st, false, "softmax tensor-core launch", mq, mk, mv, (const InT *)sp.v,
+                         sp.v_hs, sp.v_ts, p);
+}
+
+template <typename InT, typename OutT>
+la_status by_shape(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
+    const bool pair = sp.group % 2 == 0;
+    if (d == 128) {
+        if (pair) return run<InT, OutT, 128, true>(sp, dt, status, wait_ns, st);
+        return run<InT, OutT, 128, false>(sp, dt, status, wait_ns, st);
+    }
+    if (pair) return run<InT, OutT, 64, true>(sp, dt, status, wait_ns, st);
+    return run<InT, OutT, 64, false>(sp, dt, status, wait_ns, st);
+}
+
+}  // namespace
+
+la_status softmax_tc(const SoftmaxParams &sp, la_dtype in, la_dtype out, int d, int *status,
+                     unsigned long long wait_ns, cudaStream_t st) {
+    if (in == LA_BF16)
+        return out == LA_F32 ? by_shape<bf16, float>(sp, in, d, status, wait_ns, st)
+                             : by_shape<bf16, bf16>(sp, in, d, status, wait_ns, st);
+    return out == LA_F32 ? by_shape<f16, float>(sp, in, d, status, wait_ns, st)
+                         : by_shape<f16, f16>(sp, in, d, status, wait_ns, st);
+}
+
+}  // namespace la

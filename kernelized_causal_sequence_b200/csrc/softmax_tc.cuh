@@ -1,0 +1,474 @@
+// softmax_tc.cuh — causal softmax attention over packed sequences on the
+// tensor cores (bf16/fp16 inputs, head dim 64 or 128, fp32 sums).
+//
+// A CTA holds two tiles ("slots") of 128 queries that read the same keys and
+// values: the same rows of two query heads that share a key/value head where
+// heads are shared evenly (PAIR), else 256 consecutive rows of one head.  It
+// walks the keys in blocks of 128 from the sequence's begin to the tile's
+// diagonal.  Per slot and block j, with c = scale log2(e):
+//
+//   S = Q K_j^T                     tcgen05, fp32 in TMEM
+//   m' = max(m, rowmax S)           the reference of the exponents moves only
+//                                   where m' - m > 8 / c, see below
+//   P = 2^(c S - c m), l += rowsum  P rounded once to the input type, in TMEM
+//   O += P V_j                      tcgen05, fp32 in TMEM
+//   out = O / l
+//
+// Moving the reference multiplies O and l by 2^(c (m - m')).  O lives in TMEM,
+// so this is a read and a write of the whole accumulator; a reference that is
+// up to 2^8 too small costs nothing (P <= 256, and neither type's relative
+// rounding depends on it), so it is moved only beyond that: after the first
+// blocks almost never.
+//
+// The two slots alternate on the tensor core: while one slot's exponentials
+// run, the products of the other do.  With 128 x 128 scores per block the
+// exponentials (16 a clock and SM on the special-function unit) take as long
+// as both products at d 128 and twice as long at d 64, so part of them is
+// computed by a polynomial on the FMA units (exp2_poly).
+//
+// Warps (352 threads, one CTA per SM):
+//   0-3, 4-7   softmax of slot 0, 1: a thread owns one row (TMEM lane)
+//   8          TMA producer (one thread): Q, then K_0, V_0, K_1, V_1, ...
+//   9          TMEM allocation, MMA issue (one thread)
+//   10         the values of a diagonal block: rows behind the sequence are
+//              zeroed, and NaN or infinities taken out, since P = 0 does not
+//              hide them from the product; the rows that see them get them
+//              back at the end (restore_nonfinite)
+//
+// Order on the tensor core: tcgen05 products of one thread run in issue order,
+// so S of block j + 1 may overwrite the columns that hold P of block j once
+// P V_j has been issued, and a commit after S(j + 1) tells that P V_j is done
+// (which the rescaling of O relies on).
+#pragma once
+#include <type_traits>
+
+#include "packed.cuh"
+#include "softmax_simt.cuh"
+#include "tc_prefill.cuh"
+
+namespace la {
+namespace stc {
+
+using namespace tc;
+
+constexpr int kThreads = 352;
+constexpr int kBlock = 128;   // keys of a block, rows of a slot
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScrubWarp = 10;
+constexpr float kLazyLog2 = 8.f;   // how far (log2) the maximum may outgrow the reference
+
+template <int D> struct Cfg {
+    static constexpr int KB = D / 64;                  // 128-byte boxes per row
+    static constexpr int BOXB = kBlock * 128;
+    static constexpr int TILE = kBlock * D * 2;
+    static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in flight (all the shared memory there is)
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + NST * TILE;
+    static constexpr int B_Q = 0, B_KV_FULL = 2, B_KV_EMPTY = B_KV_FULL + NST, B_S = B_KV_EMPTY + NST;
+    static constexpr int B_P = B_S + 2, B_O = B_P + 2, B_CLEAN = B_O + 2;
+    // a diagonal block's values have a full barrier of their own: the scrub warp
+    // does not follow the ring's phases (they are the last use of their stages)
+    static constexpr int B_VD = B_CLEAN + 2, B_DRAIN = B_VD + 2;
+    static constexpr int NBAR = B_DRAIN + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM + 4;
+    static constexpr int OFF_FLAG = OFF_ABORT + 4;     // two ints: a diagonal block held NaN or infinities
+    static constexpr int SMEM = OFF_FLAG + 8 + 1024;   // + alignment
+    static constexpr int T_S = 0, T_O = 256;           // TMEM: S / P of slot s at 128 s, O at 256 + 128 s
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct Params {
+    void *out;
+    const int32_t *cu;
+    long o_hs, o_ts;
+    int H, group, N, n_seq, tiles;
+    float scale_log2;
+    int *status;
+    unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <typename InT> __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (std::is_same<InT, bf16>::value) return pack_bf16x2(lo, hi);
+    else return pack_f16x2(lo, hi);
+}
+
+// x * 0 + acc for a packed pair: NaN stays behind for any NaN or infinity.
+template <typename InT> __device__ __forceinline__ uint32_t probe2(uint32_t x, uint32_t acc) {
+    uint32_t r;
+    if constexpr (std::is_same<InT, bf16>::value) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
+template <typename InT> __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t x) {
+    constexpr uint32_t E = std::is_same<InT, bf16>::value ? 0x7F80u : 0x7C00u;
+    if ((x & E) == E) x &= 0xFFFF0000u;
+    if (((x >> 16) & E) == E) x &= 0x0000FFFFu;
+    return x;
+}
+
+// A diagonal block's value tile [KB boxes][128 rows][128 B]: rows at or past n
+// are zeroed, NaN and infinities become 0 (returns whether there were any).
+// One warp.
+template <typename InT, int D> __device__ __noinline__ bool scrub_values(uint8_t *tile, int n, int lane) {
+    constexpr int CH = Cfg<D>::TILE / 16;   // 16-byte chunks; chunk i of box b, row r: b * 1024 + r * 8 + i
+    uint32_t acc = 0u;
+#pragma unroll 8
+    for (int i = lane; i < CH; i += 32) {
+        uint4 *p = reinterpret_cast<uint4 *>(tile) + i;
+        if ((i & 1023) / 8 >= n) {
+            *p = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            const uint4 x = *p;
+            acc = probe2<InT>(x.x, acc);
+            acc = probe2<InT>(x.y, acc);
+            acc = probe2<InT>(x.z, acc);
+            acc = probe2<InT>(x.w, acc);
+        }
+    }
+    constexpr uint32_t E = std::is_same<InT, bf16>::value ? 0x7F80u : 0x7C00u;
+    const bool bad = __any_sync(0xffffffffu, (acc & E) == E || ((acc >> 16) & E) == E);
+    if (bad) {
+        for (int i = lane; i < CH; i += 32) {
+            uint4 *p = reinterpret_cast<uint4 *>(tile) + i;
+            const uint4 x = *p;
+            *p = make_uint4(finite_or_zero2<InT>(x.x), finite_or_zero2<InT>(x.y), finite_or_zero2<InT>(x.z),
+                            finite_or_zero2<InT>(x.w));
+        }
+    }
+    return bad;
+}
+
+// Adds the NaN and infinities of values j0 .. min(j1, row) to this thread's
+// row of O (p > 0 times infinity is infinity).  Rare; whole warp.
+template <typename InT, int D>
+__device__ __noinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long ts, int j0, int j1, int row) {
+    for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t u[32];
+        tmem_ld32(t_o + cb * 32, u);
+        tmem_ld_wait();
+        for (int j = j0; j < j1; ++j) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float x = to_f32<InT>(v[(long)j * ts + cb * 32 + i]);
+                if (j <= row && !isfinite(x)) u[i] = __float_as_uint(__uint_as_float(u[i]) + x);
+            }
+        }
+        tmem_st32(t_o + cb * 32, u);
+    }
+    tmem_st_wait();
+}
+
+template <typename InT, typename OutT, int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const InT *__restrict__ v_gmem, long v_hs, long v_ts,
+                  const Params p) {
+    using G = Cfg<D>;
+    extern __shared__ uint8_t stc_smem_raw[];
+    uint8_t *smem = stc_smem_raw + ((1024u - (smem_u32(stc_smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + G::OFF_BAR);
+    uint32_t *tmem_addr = reinterpret_cast<uint32_t *>(smem + G::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + G::OFF_ABORT);
+    volatile int *flag = reinterpret_cast<volatile int *>(smem + G::OFF_FLAG);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the work: heads fastest (CTAs that run together share keys), late tiles,
+    // which have the most keys, first
+    const int nhp = PAIR ? p.H / 2 : p.H;
+    const int hp = blockIdx.x % nhp, tile = p.tiles - 1 - blockIdx.x / nhp;
+    const SeqTile t = seq_tile<PAIR ? 128 : 256>(p.cu, p.n_seq, p.N, tile);
+    if (t.q0 >= t.end) return;
+    const int h0 = PAIR ? 2 * hp : hp, hk = h0 / p.group;
+    // blocks of each slot; the last is the diagonal one
+    const int n0 = (t.q0 - t.begin) / kBlock + 1;
+    const int n1 = PAIR ? n0 : (t.q0 + kBlock < t.end ? n0 + 1 : 0);
+    const int nb = max(n0, n1);
+    const int n_diag = n1 > n0 ? 2 : 1;   // diagonal blocks: n0 - 1 and, with two row tiles, n0
+
+    AbortCtx ab{abort_flag, p.status, p.wait_ns};
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        flag[0] = flag[1] = 0;
+        for (int i = 0; i < G::NBAR; ++i) mbar_init(&bar[i], (i == G::B_P || i == G::B_P + 1) ? 4 : 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_addr, 512);
+    if (warp == kTmaWarp && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_addr;
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int s = 0; s < 2; ++s) {
+                if (s == 1 && n1 == 0) continue;
+                mbar_expect_tx(&bar[G::B_Q + s], G::TILE);
+                for (int b = 0; b < G::KB; ++b)
+                    tma_load_3d(smem + G::OFF_Q + s * G::TILE + b * G::BOXB, &tm_q, &bar[G::B_Q + s], 64 * b,
+                                PAIR ? t.q0 : t.q0 + s * kBlock, PAIR ? h0 + s : h0);
+                // K_0 between the two: the first product needs Q of slot 0 and K_0
+                if (s == 0) {
+                    mbar_expect_tx(&bar[G::B_KV_FULL], G::TILE);
+                    for (int b = 0; b < G::KB; ++b)
+                        tma_load_3d(smem + G::OFF_KV + b * G::BOXB, &tm_k, &bar[G::B_KV_FULL], 64 * b, t.begin, hk);
+                    issued = 1;
+                }
+            }
+            for (int i = 1; i < 2 * nb; ++i) {
+                const int st = i % G::NST, use = i / G::NST;
+                if (use > 0 && !mbar_wait(&bar[G::B_KV_EMPTY + st], (use - 1) & 1, ab, 1)) break;
+                const int dg = (i >> 1) - (n0 - 1);
+                uint64_t *full = &bar[(i & 1) && dg >= 0 ? G::B_VD + dg : G::B_KV_FULL + st];
+                mbar_expect_tx(full, G::TILE);
+                issued = i + 1;
+                for (int b = 0; b < G::KB; ++b)
+                    tma_load_3d(smem + G::OFF_KV + st * G::TILE + b * G::BOXB, (i & 1) ? &tm_v : &tm_k, full, 64 * b,
+                                t.begin + (i >> 1) * kBlock, hk);
+            }
+            // every copy issued has completed before the CTA exits (each is waited
+            // for by its reader too, unless that gave up)
+            volatile int never = 0;
+            AbortCtx timed{&never, nullptr, kDrainLimitNs};
+            mbar_wait(&bar[G::B_Q], 0, timed, 0);
+            if (n1 > 0) mbar_wait(&bar[G::B_Q + 1], 0, timed, 0);
+            for (int i = max(0, issued - G::NST); i < issued; ++i) {
+                const int dg = (i >> 1) - (n0 - 1);
+                if ((i & 1) && dg >= 0) mbar_wait(&bar[G::B_VD + dg], 0, timed, 0);
+                else mbar_wait(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, timed, 0);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr bool BF = std::is_same<InT, bf16>::value;
+            constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
+            constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
+            const uint32_t sb = smem_u32(smem);
+            auto full = [&](int i) { return mbar_wait(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, ab, 2); };
+            auto product_s = [&](int s, int j) {
+                const uint64_t a = sdesc_sw128(sb + G::OFF_Q + s * G::TILE, 16, 1024);
+                const uint64_t b = sdesc_sw128(sb + G::OFF_KV + (2 * j % G::NST) * G::TILE, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * G::BOXB + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + G::T_S + 128 * s, a + off, b + off, ID_S, kk > 0);
+                }
+                mma_commit(&bar[G::B_S + s]);
+            };
+            bool ok = full(0);
+            for (int s = 0; s < 2 && ok; ++s) {
+                if (s == 1 && n1 == 0) continue;
+                ok = mbar_wait(&bar[G::B_Q + s], 0, ab, 3);
+                if (!ok) break;
+                tc_fence_after();
+                product_s(s, 0);
+            }
+            if (ok) mma_commit(&bar[G::B_KV_EMPTY]);
+            for (int j = 0; j < nb && ok; ++j) {
+                const int st_v = (2 * j + 1) % G::NST, st_k = (2 * j + 2) % G::NST;
+                for (int s = 0; s < 2 && ok; ++s) {
+                    const int n = s ? n1 : n0;
+                    if (j >= n) continue;
+                    ok = (j < n0 - 1 ? full(2 * j + 1) : mbar_wait(&bar[G::B_CLEAN + j - (n0 - 1)], 0, ab, 4)) &&
+                         mbar_wait(&bar[G::B_P + s], j & 1, ab, 5);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t bv = sdesc_sw128(sb + G::OFF_KV + st_v * G::TILE, G::BOXB, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kBlock / 16; ++kk)
+                        mma_ts(tmem + G::T_O + 128 * s, tmem + G::T_S + 128 * s + kk * 8,
+                               bv + (uint64_t)((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                    if (j == n - 1) mma_commit(&bar[G::B_O + s]);
+                    if (j + 1 < n) {
+                        ok = full(2 * j + 2);
+                        if (!ok) break;
+                        product_s(s, j + 1);
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&bar[G::B_KV_EMPTY + st_v]);
+                if (j + 1 < nb) mma_commit(&bar[G::B_KV_EMPTY + st_k]);
+            }
+            // every product issued has completed before TMEM is freed
+            volatile int never = 0;
+            AbortCtx timed{&never, nullptr, kDrainLimitNs};
+            mma_commit(&bar[G::B_DRAIN]);
+            mbar_wait(&bar[G::B_DRAIN], 0, timed, 0);
+        }
+    } else if (warp == kScrubWarp) {
+        for (int b = 0; b < n_diag; ++b) {
+            const int j = n0 - 1 + b, i = 2 * j + 1;
+            if (!mbar_wait(&bar[G::B_VD + b], 0, ab, 6)) break;
+            const int n = t.end - (t.begin + j * kBlock);   // rows of the sequence
+            if (scrub_values<InT, D>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane) && lane == 0) flag[b] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[G::B_CLEAN + b]);
+        }
+    } else {
+        // softmax of slot s: thread = row
+        const int s = warp >> 2, q = warp & 3;
+        const int n = s ? n1 : n0;
+        const int q0 = PAIR ? t.q0 : t.q0 + s * kBlock;
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + G::T_S + 128 * s, t_o = tmem + lane_base + G::T_O + 128 * s;
+        const int r = q * 32 + lane;
+        const float c = p.scale_log2;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            ok = mbar_wait(&bar[G::B_S + s], j & 1, ab, 7);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t u[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, u[i]);
+            tmem_ld_wait();
+            if (j == n - 1) {
+                // diagonal block: keys up to the row's own and within the sequence
+                // (rows behind the sequence see its last key: their results are dropped)
+                const int last = min(r, t.end - 1 - q0);
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i > last) u[i / 32][i % 32] = 0xff800000u;
+            }
+            float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i / 32][i % 32]));
+            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (j == 0) {
+                m = mn;
+            } else {
+                const bool move = (mn - m) * c > kLazyLog2;   // (m = -inf: infinite; mn = -inf: NaN, false)
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? ex2_approx((m - mn) * c) : 1.f;
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + cb * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(t_o + cb * 32, o);
+                    }
+                    l *= f;
+                    m = move ? mn : m;
+                }
+            }
+            const float neg = m == -INFINITY ? 0.f : -m * c;
+            const uint64_t c2 = pack2(c, c), n2 = pack2(neg, neg);
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int e = g * 64 + 2 * i;
+                    float a, b;
+                    unpack2(fma2(pack2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])), c2, n2), a, b);
+                    a = ex2_approx(a);
+                    b = ex2_approx(b);
+                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+                    w[i] = pack16<InT>(a, b);
+                }
+                tmem_st32(t_s + 32 * g, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[G::B_P + s]);
+            float s0, s1, s2, s3;
+            unpack2(sum[0], s0, s1);
+            unpack2(sum[1], s2, s3);
+            l += (s0 + s1) + (s2 + s3);
+        }
+        if (ok && n > 0) ok = mbar_wait(&bar[G::B_O + s], 0, ab, 8);
+        if (ok && n > 0) {
+            tc_fence_after();
+            const int row = q0 + r;
+            for (int b = 0; b < n_diag; ++b)
+                if (flag[b]) {
+                    const int j0 = t.begin + (n0 - 1 + b) * kBlock;
+                    restore_nonfinite<InT, D>(t_o, v_gmem + hk * v_hs, v_ts, j0, min(j0 + kBlock, t.end), row);
+                }
+            // O / l through this warp's rows of the slot's query tile (no product
+            // reads it any more) to whole-row stores
+            const float inv = 1.f / l;
+            constexpr int RB = D * 2, CPR = RB / 16;        // bytes, 16-byte chunks of a staged row
+            constexpr int PASS = sizeof(OutT) == 4 ? 2 : 1;
+            uint8_t *stg = smem + G::OFF_Q + s * G::TILE + q * 32 * RB;
+            OutT *out = (OutT *)p.out + (long)(PAIR ? h0 + s : h0) * p.o_hs;
+#pragma unroll 1
+            for (int ps = 0; ps < PASS; ++ps) {
+#pragma unroll
+                for (int cb = 0; cb < D / 32 / PASS; ++cb) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + ps * (D / 2) + cb * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                    if constexpr (PASS == 1) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint4 w;
+                            uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                wp[y] = pack16<InT>(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
+                            *reinterpret_cast<uint4 *>(stg + lane * RB + (((cb * 4 + x) ^ (lane & 7)) << 4)) = w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint4 *>(stg + lane * RB + (((cb * 8 + x) ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int i = lane; i < 32 * CPR; i += 32) {
+                    const int rr = i / CPR, ch = i % CPR;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(stg + rr * RB + ((ch ^ (rr & 7)) << 4));
+                    const int row_g = q0 + q * 32 + rr;
+                    if (row_g < t.end)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(out + (long)row_g * p.o_ts) + ps * RB + ch * 16) = w;
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace stc
+}  // namespace la
