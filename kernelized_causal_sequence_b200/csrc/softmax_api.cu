@@ -125,34 +125,27 @@ template <typename OutT> la_status run_read(const Kv4AppendParams &p, int d, cud
     LA_BY_D(d, return launch_kernel(kv4_read_kernel<OutT, D>, grid, dim3(kAppendThreads), 0, st, true,
                                     "kv4 read launch", p))
 }
-// The split of a sequence over CTAs (kDecWarps warps each, a few CTAs per SM).
-// Lengths are known on the device only, so the split goes by the capacity:
-// enough splits that a batch filled to half of it keeps every SM's CTAs busy
-// for a few rounds (ragged lengths even out over them), but none shorter than
-// what hides a CTA's start (kDecMinSplit positions).
-constexpr int kDecMinSplit = 256, kDecCtasPerSm = 3;
+// CTAs of the decode kernel: as many as are resident at once (its launch
+// bounds), or one per row for short caches.
 struct DecodePlan {
-    int nt, head_blocks, n_split, split_len;
-    size_t ml_off, o_off, scores_off, bytes;
+    int nt, head_blocks, n_cta, whole;
+    size_t ml_off, o_off, row_off, scores_off, bytes;
 };
 DecodePlan decode_plan(int B, int H, int H_kv, int cap, int d, int with_weights) {
     DecodePlan w;
     const int group = H / H_kv;
     w.nt = group > 8 ? 2 : 1;
     w.head_blocks = (group + 8 * w.nt - 1) / (8 * w.nt);
+    w.whole = cap <= kDecWhole;
     const long rows = (long)B * H_kv * w.head_blocks;
-    const long want = 4L * kNumSMs * kDecCtasPerSm;   // CTAs at full capacity
-    long len = ((long)cap * rows + want - 1) / want;
-    len = (len + kDecTile * kDecWarps - 1) / (kDecTile * kDecWarps) * (kDecTile * kDecWarps);
-    if (len < kDecMinSplit) len = kDecMinSplit;
-    w.split_len = (int)len;
-    w.n_split = (int)((cap + len - 1) / len);
-    if (w.n_split < 1) w.n_split = 1;
-    const bool parts = w.n_split > 1;
-    w.ml_off = 0;
-    size_t at = parts || with_weights ? ws_up((size_t)B * H * w.n_split * sizeof(float2)) : 0;
+    w.n_cta = w.whole ? (int)rows : kNumSMs * (w.nt == 1 ? kDecCtas : 2);
+    size_t at = 0;
+    w.ml_off = at;
+    if (!w.whole) at += ws_up((size_t)2 * w.n_cta * 8 * w.nt * sizeof(float2));
     w.o_off = at;
-    if (parts) at += ws_up((size_t)B * H * w.n_split * d * sizeof(float));
+    if (!w.whole) at += ws_up((size_t)2 * w.n_cta * 8 * w.nt * d * sizeof(float));
+    w.row_off = at;
+    if (with_weights) at += ws_up((size_t)B * H * sizeof(float2));
     w.scores_off = at;
     if (with_weights) at += ws_up((size_t)B * H * cap * sizeof(float));
     w.bytes = at;
@@ -161,12 +154,11 @@ DecodePlan decode_plan(int B, int H, int H_kv, int cap, int d, int with_weights)
 
 template <typename InT, typename OutT, int D, int NT>
 la_status run_decode_nt(const Kv4DecodeParams &p, cudaStream_t st) {
-    la_status s = launch_kernel(kv4_decode_kernel<InT, OutT, D, NT>,
-                                dim3((unsigned)p.n_split, (unsigned)(p.c.Hkv * p.head_blocks), (unsigned)p.c.B),
-                                dim3(kDecWarps * 32), kv4_decode_smem<D>(NT), st, true, "kv4 decode launch", p);
-    if (s != LA_OK || (p.n_split == 1 && !p.weights_out)) return s;
+    la_status s = launch_kernel(kv4_decode_kernel<InT, OutT, D, NT>, dim3((unsigned)p.n_cta), dim3(kDecWarps * 32),
+                                kv4_decode_smem<D>(NT), st, true, "kv4 decode launch", p);
+    if (s != LA_OK || (p.whole && !p.weights_out)) return s;
     constexpr int HPB = kFinThreads / (D / 4);
-    const unsigned ob = p.n_split > 1 ? (unsigned)((p.group + HPB - 1) / HPB) : 0u;
+    const unsigned ob = p.whole ? 0u : (unsigned)((p.group + HPB - 1) / HPB);
     const unsigned wb = p.weights_out ? stride_grid(p.c.cap, kFinThreads, (long)p.c.Hkv * p.c.B) : 0u;
     return launch_kernel(kv4_finish_kernel<OutT, D>, dim3(ob + wb, (unsigned)p.c.Hkv, (unsigned)p.c.B),
                          dim3(kFinThreads), 0, st, true, "kv4 finish launch", p, (int)ob);
@@ -260,7 +252,7 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
 }
 
 size_t la_kv4_decode_workspace_size(int B, int H, int H_kv, int cap, int d, int with_weights) {
-    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv || cap <= 0 || cap > kMaxTokens || !d_ok(d)) return 0;
+    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv || cap < 0 || cap > kMaxTokens || !d_ok(d)) return 0;
     return decode_plan(B, H, H_kv, cap, d, with_weights).bytes;
 }
 
@@ -279,22 +271,25 @@ la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_ca
     if (weights_in != weights_out && overlap(weights_in, wb, weights_out, wb)) return LA_ERR_INVALID_ARG;
     const DecodePlan pl = decode_plan(cache->B, H, cache->H_kv, cache->cap, cache->d, weights_out != nullptr);
     if (!ws_ok(workspace, workspace_bytes, pl.bytes)) return LA_ERR_INVALID_ARG;
-    if ((long)cache->H_kv * pl.head_blocks > 65535) return LA_ERR_UNSUPPORTED;
+    if ((long)cache->B * cache->H_kv * pl.head_blocks > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
     char *ws = (char *)workspace;
     Kv4DecodeParams p;
     std::memset(&p, 0, sizeof(p));
     p.q = q; p.c = dev_cache(cache); p.lens = lens; p.weights_in = weights_in; p.weights_out = weights_out;
     p.out = out; p.H = H; p.group = H / cache->H_kv; p.scale_log2 = scale * kLog2e;
-    p.n_split = pl.n_split; p.split_len = pl.split_len; p.head_blocks = pl.head_blocks;
-    if (pl.n_split > 1 || weights_out) p.part_ml = (float2 *)(ws + pl.ml_off);
-    if (pl.n_split > 1) p.part_o = (float *)(ws + pl.o_off);
-    if (weights_out) p.scores = (float *)(ws + pl.scores_off);
+    p.n_cta = pl.n_cta; p.whole = pl.whole; p.head_blocks = pl.head_blocks; p.head_block = 8 * pl.nt;
+    p.part_ml = (float2 *)(ws + pl.ml_off);
+    p.part_o = (float *)(ws + pl.o_off);
+    if (weights_out) {
+        p.row_ml = (float2 *)(ws + pl.row_off);
+        p.scores = (float *)(ws + pl.scores_off);
+    }
     cudaStream_t st = (cudaStream_t)stream;
     LA_BY_TYPES(in_dtype, out_dtype, return (run_decode<InT, OutT>(p, cache->d, pl.nt, st)))
 }
 
 size_t la_kv4_evict_workspace_size(int B, int H_kv, int cap, int keep) {
-    if (B <= 0 || H_kv <= 0 || cap <= 0 || cap > kMaxTokens || keep < 1) return 0;
+    if (B <= 0 || H_kv <= 0 || cap < 0 || cap > kMaxTokens || keep < 1) return 0;
     return ws_up((size_t)B * H_kv * keep * sizeof(int32_t));
 }
 
