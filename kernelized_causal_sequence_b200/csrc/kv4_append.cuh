@@ -55,6 +55,7 @@ template <typename InT, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendParams p) {
     constexpr int G = D / kKv4Group;
     using Chunk = typename Kv4Chunk<D>::type;
+    pdl_wait();
     const int r = threadIdx.x & 7, head = blockIdx.y;
     const bool keys = blockIdx.z == 0;
     const InT *x = keys ? (const InT *)p.k + head * p.k_hs : (const InT *)p.v + head * p.v_hs;
@@ -66,36 +67,44 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendPar
     for (int t0 = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 5) * 4; t0 < p.N; t0 += step) {
         const int t = t0 + ((threadIdx.x & 31) >> 3);
         const long row = t < p.N ? kv4_row(p, t, head) : -1;
-        float v[G][4];
-        uint32_t word = 0;
+        float v[G][4], lo[G], hi[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (row >= 0) f = load4<InT>(x + (long)t * ts + g * kKv4Group + r * 4);
             v[g][0] = f.x; v[g][1] = f.y; v[g][2] = f.z; v[g][3] = f.w;
-            float lo = fminf(fminf(f.x, f.y), fminf(f.z, f.w)), hi = fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w));
-            // magnitudes as bits: a NaN or an infinity is the largest
-            uint32_t a = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(v[g][i]) & 0x7fffffffu);
-#pragma unroll
-            for (int off = 4; off > 0; off >>= 1) {
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-                a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-            }
-            // thread g of the eight forms group g's word (its float64 divisions once per group)
-            if (r == g) word = kv4_word(lo, hi, a);
+            lo[g] = min_nan(min_nan(f.x, f.y), min_nan(f.z, f.w));
+            hi[g] = max_nan(max_nan(f.x, f.y), max_nan(f.z, f.w));
         }
+        // over the eight threads; with several groups each step also halves
+        // the groups that a thread goes on with (4: 8 shuffles instead of 24):
+        // thread r ends with group (r / 4) G / 2 + (r / 2) % 2 (G / 4) ...
+#pragma unroll
+        for (int off = 4, n = G; off > 0; off >>= 1) {
+            if (n > 1) {
+                const bool up = r & off;
+                n >>= 1;
+#pragma unroll
+                for (int g = 0; g < n; ++g) {
+                    const float l = __shfl_xor_sync(0xffffffffu, up ? lo[g] : lo[g + n], off);
+                    const float h = __shfl_xor_sync(0xffffffffu, up ? hi[g] : hi[g + n], off);
+                    lo[g] = min_nan(up ? lo[g + n] : lo[g], l);
+                    hi[g] = max_nan(up ? hi[g + n] : hi[g], h);
+                }
+            } else {
+                lo[0] = min_nan(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], off));
+                hi[0] = max_nan(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], off));
+            }
+        }
+        // the word of that group (NaN in lo and hi if any value was)
+        const uint32_t own = kv4_word(lo[0], hi[0], __float_as_uint(max_nan(fabsf(lo[0]), fabsf(hi[0]))) & 0x7fffffffu);
+        uint32_t word = 0u;   // group r's, for the store
         Chunk chunk = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const uint32_t w = __shfl_sync(0xffffffffu, word, g, 8);
-            const float sc = kv4_scale(w), of = kv4_offset(w), inv = 1.f / sc;
-            uint32_t f = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f |= kv4_code(v[g][i], sc, inv, of) << (4 * i);
-            chunk |= (Chunk)((Chunk)f << (16 * g));
+            const uint32_t w = __shfl_sync(0xffffffffu, own, g * (8 / G), 8);
+            if (r == g) word = w;
+            chunk |= (Chunk)((Chunk)kv4_codes(v[g], w) << (16 * g));
         }
         if (row >= 0) {
             reinterpret_cast<Chunk *>(codes)[row * 8 + r] = chunk;

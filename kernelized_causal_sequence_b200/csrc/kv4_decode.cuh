@@ -710,58 +710,101 @@ __global__ void __launch_bounds__(kFinThreads) kv4_finish_kernel(const Kv4Decode
         }
         return x;
     };
+    // log2 of a row's denominator, and its greatest reference; the pieces over a warp's lanes
+    auto join = [&](const DecPieces &x, int head, float *top) {
+        const int lane = threadIdx.x & 31;
+        float M_ = -INFINITY, L = 0.f;
+        for (int c = x.first + lane; c <= x.last; c += 32) {
+            const float2 ml = p.part_ml[x.slot(c) * HB + head % HB];
+            const float M2 = fmaxf(M_, ml.x);
+            if (M2 > -INFINITY) L = L * ex2_approx(M_ - M2) + ml.y * ex2_approx(ml.x - M2);
+            else L += ml.y;
+            M_ = M2;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, M_, off), l2 = __shfl_xor_sync(0xffffffffu, L, off);
+            const float M2 = fmaxf(M_, m2);
+            if (M2 > -INFINITY) L = L * ex2_approx(M_ - M2) + l2 * ex2_approx(m2 - M2);
+            else L += l2;
+            M_ = M2;
+        }
+        *top = M_;
+        return L;
+    };
+    __shared__ float lse[kFinThreads];
+    __shared__ float part[kFinThreads * 4];
     if ((int)blockIdx.x < out_blocks) {
-        constexpr int TPH = D / 4, HPB = kFinThreads / TPH;   // threads of a head, heads of a block
-        const int i = blockIdx.x * HPB + threadIdx.x / TPH, c4 = threadIdx.x % TPH;
-        if (i >= p.group) return;
+        // one head per block: its pieces over the threads' rows, each thread four channels
+        constexpr int TPH = D / 4, ROWS = kFinThreads / TPH;
+        const int i = blockIdx.x, c4 = threadIdx.x % TPH, k = threadIdx.x / TPH;
         const DecPieces x = pieces(i);
         if (x.first == x.last) return;
-        float M_ = -INFINITY, L = 0.f;
-        for (int c = x.first; c <= x.last; ++c) M_ = fmaxf(M_, p.part_ml[x.slot(c) * HB + i % HB].x);
+        float M_;
+        const float L = join(x, i, &M_);
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int c = x.first; c <= x.last; ++c) {
+        for (int c = x.first + k; c <= x.last; c += ROWS) {
             const long at = (long)x.slot(c) * HB + i % HB;
-            const float2 ml = p.part_ml[at];
-            const float f = M_ == -INFINITY ? 1.f : ex2_approx(ml.x - M_);
+            const float f = M_ == -INFINITY ? 1.f : ex2_approx(p.part_ml[at].x - M_);
             const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + c4 * 4);
-            L = fmaf(ml.y, f, L);
             a.x = fmaf(v.x, f, a.x); a.y = fmaf(v.y, f, a.y); a.z = fmaf(v.z, f, a.z); a.w = fmaf(v.w, f, a.w);
         }
-        const float inv = 1.f / L;
-        store4<OutT>((OutT *)p.out + (h0 + i) * D + c4 * 4, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        reinterpret_cast<float4 *>(part)[threadIdx.x] = a;
+        __syncthreads();
+        if (k == 0) {
+#pragma unroll
+            for (int y = 1; y < ROWS; ++y) {
+                const float4 v = reinterpret_cast<const float4 *>(part)[y * TPH + c4];
+                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+            }
+            const float inv = 1.f / L;
+            store4<OutT>((OutT *)p.out + (h0 + i) * D + c4 * 4, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        }
         return;
     }
     // weights_out[t] = weights_in[t] + sum over the group's heads of 2^(score - lse)
-    __shared__ float lse[kFinThreads];
     const long row0 = ((long)b * p.c.Hkv + hk) * p.c.cap;
     const int wb = blockIdx.x - out_blocks, nwb = gridDim.x - out_blocks;
     for (int i0 = 0; i0 < p.group; i0 += kFinThreads) {
         __syncthreads();
         const int gi = min(kFinThreads, p.group - i0);
-        if ((int)threadIdx.x < gi) {
-            const int i = i0 + threadIdx.x;
-            const DecPieces x = pieces(i);
-            float M_ = -INFINITY, L = 0.f;
+        for (int i = threadIdx.x / 32; i < gi; i += kFinThreads / 32) {
+            const DecPieces x = pieces(i0 + i);
+            float M_, L;
             if (x.first == x.last) {
-                M_ = p.row_ml[h0 + i].x;
-                L = p.row_ml[h0 + i].y;
+                const float2 ml = p.row_ml[h0 + i0 + i];
+                M_ = ml.x;
+                L = ml.y;
             } else {
-                for (int c = x.first; c <= x.last; ++c) M_ = fmaxf(M_, p.part_ml[x.slot(c) * HB + i % HB].x);
-                for (int c = x.first; c <= x.last; ++c) {
-                    const float2 ml = p.part_ml[x.slot(c) * HB + i % HB];
-                    L += ml.y * (M_ == -INFINITY ? 1.f : ex2_approx(ml.x - M_));
-                }
+                L = join(x, i0 + i, &M_);
             }
-            lse[threadIdx.x] = M_ + log2f(L);
+            if ((threadIdx.x & 31) == 0) lse[i] = M_ + log2f(L);
         }
         __syncthreads();
-        for (int t = wb * kFinThreads + threadIdx.x; t < n; t += nwb * kFinThreads) {
-            float w = i0 > 0 ? p.weights_out[row0 + t] : p.weights_in ? p.weights_in[row0 + t] : 0.f;
-            float sum = 0.f;
+        // four positions a thread where the rows are aligned for it
+        const bool four = (p.c.cap & 3) == 0;
+        const int per = four ? 4 : 1;
+        for (int t = (wb * kFinThreads + threadIdx.x) * per; t < n; t += nwb * kFinThreads * per) {
+            const float *from = i0 > 0 ? p.weights_out : p.weights_in;
+            if (four && t + 4 <= n) {
+                float4 w = from ? *reinterpret_cast<const float4 *>(from + row0 + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int i = 0; i < gi; ++i) sum += ex2_approx(p.scores[(h0 + i0 + i) * p.c.cap + t] - lse[i]);
-            p.weights_out[row0 + t] = w + sum;
+                for (int i = 0; i < gi; ++i) {
+                    const float4 s = *reinterpret_cast<const float4 *>(p.scores + (h0 + i0 + i) * p.c.cap + t);
+                    sum.x += ex2_approx(s.x - lse[i]); sum.y += ex2_approx(s.y - lse[i]);
+                    sum.z += ex2_approx(s.z - lse[i]); sum.w += ex2_approx(s.w - lse[i]);
+                }
+                *reinterpret_cast<float4 *>(p.weights_out + row0 + t) =
+                    make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+            } else {
+                for (int u = t; u < min(t + per, n); ++u) {
+                    float sum = 0.f;
+                    for (int i = 0; i < gi; ++i) sum += ex2_approx(p.scores[(h0 + i0 + i) * p.c.cap + u] - lse[i]);
+                    p.weights_out[row0 + u] = (from ? from[row0 + u] : 0.f) + sum;
+                }
+            }
         }
     }
 }

@@ -117,7 +117,7 @@ la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
     const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
-    LA_BY_D(d, return launch_kernel(kv4_append_kernel<InT, D>, grid, dim3(kAppendThreads), 0, st, false,
+    LA_BY_D(d, return launch_kernel(kv4_append_kernel<InT, D>, grid, dim3(kAppendThreads), 0, st, true,
                                     "kv4 append launch", p))
 }
 template <typename OutT> la_status run_read(const Kv4AppendParams &p, int d, cudaStream_t st) {
@@ -157,15 +157,21 @@ la_status run_decode_nt(const Kv4DecodeParams &p, cudaStream_t st) {
     la_status s = launch_kernel(kv4_decode_kernel<InT, OutT, D, NT>, dim3((unsigned)p.n_cta), dim3(kDecWarps * 32),
                                 kv4_decode_smem<D>(NT), st, true, "kv4 decode launch", p);
     if (s != LA_OK || (p.whole && !p.weights_out)) return s;
-    constexpr int HPB = kFinThreads / (D / 4);
-    const unsigned ob = p.whole ? 0u : (unsigned)((p.group + HPB - 1) / HPB);
-    const unsigned wb = p.weights_out ? stride_grid(p.c.cap, kFinThreads, (long)p.c.Hkv * p.c.B) : 0u;
+    const unsigned ob = p.whole ? 0u : (unsigned)p.group;
+    // (four positions a thread, at most four blocks per SM)
+    const unsigned wb = p.weights_out ? stride_grid(p.c.cap, 4 * kFinThreads, 2L * p.c.Hkv * p.c.B) : 0u;
     return launch_kernel(kv4_finish_kernel<OutT, D>, dim3(ob + wb, (unsigned)p.c.Hkv, (unsigned)p.c.B),
                          dim3(kFinThreads), 0, st, true, "kv4 finish launch", p, (int)ob);
 }
 template <typename InT, typename OutT> la_status run_decode(const Kv4DecodeParams &p, int d, int nt, cudaStream_t st) {
     if (nt == 1) { LA_BY_D(d, return (run_decode_nt<InT, OutT, D, 1>(p, st))) }
     LA_BY_D(d, return (run_decode_nt<InT, OutT, D, 2>(p, st)))
+}
+
+template <int THREADS> la_status run_evict(const Kv4EvictParams &p, int d, long rows, int cs, cudaStream_t st) {
+    if (rows * cs > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
+    LA_BY_D(d, return launch_cluster(kv4_evict_kernel<D, THREADS>, dim3((unsigned)(rows * cs)), dim3(THREADS), 0, st, true, cs,
+                                     "kv4 evict launch", p, cs))
 }
 
 }  // namespace
@@ -322,12 +328,14 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     p.recent = recent; p.out_weights = out_weights; p.kept = kept; p.out_lens = out_lens;
     p.list = (int32_t *)workspace;
     cudaStream_t st = (cudaStream_t)stream;
-    s = launch_kernel(kv4_select_kernel, dim3((unsigned)cache->H_kv, (unsigned)cache->B), dim3(kEvictThreads), 0, st,
-                      false, "kv4 select launch", p);
-    if (s != LA_OK || cache->cap == 0) return s;
-    const dim3 grid(stride_grid(keep < cache->cap ? keep : cache->cap, 32, (long)cache->H_kv * cache->B),
-                    (unsigned)cache->H_kv, (unsigned)cache->B);
-    LA_BY_D(cache->d, return launch_kernel(kv4_gather_kernel<D>, grid, dim3(256), 0, st, true, "kv4 gather launch", p))
+    // short caches: small blocks, whose barriers are cheaper; long ones: as many CTAs
+    // of a (sequence, head) as its positions fill with 8 keys a thread and the
+    // machine has SMs for
+    const long rows = (long)cache->B * cache->H_kv;
+    if (cache->cap <= 256 * kEvictKeys) return run_evict<256>(p, cache->d, rows, 1, st);
+    int cs = 1;
+    while (cs < kEvictMaxCluster && (long)cs * 1024 * kEvictKeys < cache->cap && rows * cs < kNumSMs) cs *= 2;
+    return run_evict<1024>(p, cache->d, rows, cs, st);
 }
 
 }  // extern "C"
