@@ -21,6 +21,7 @@ raises: there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import typing
 
@@ -386,7 +387,9 @@ def la_decode_step(q, k, v, state_S, state_z, decay=None, eps=1e-6, out=None, ou
 #
 # These functions check what the C ABI cannot see (shapes, types, devices) and
 # raise ValueError before anything is launched.  A call runs on ``stream``, or
-# on the current stream of its tensors' device.
+# on the current stream of its tensors' device.  (A decode step is a few
+# microseconds on the GPU, so the checks are written to be cheap: plain
+# conditions, messages formed only on failure.)
 
 class KV4Cache(typing.NamedTuple):
     """A key/value cache in 4 bits (the format: la_kv4_cache in linattn.h).
@@ -408,57 +411,72 @@ class KV4Cache(typing.NamedTuple):
         return cls(*half(), *half())
 
 
+_DIMS = (32, 64, 128)
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _cache_c(cache, what="cache"):
+    """The C view of a cache and its device index."""
     kc, kp, vc, vp = cache
-    _need(kc.dim() == 4 and kc.dtype == torch.uint8 and kc.is_cuda, f"{what}.k_codes: [B, H_kv, cap, d / 2] uint8 on CUDA")
-    B, Hk, cap, half = kc.shape
-    d = half * 2
-    _need(d in (32, 64, 128), f"{what}: head dim 32, 64 or 128, not {d}")
-    _need(vc.shape == kc.shape and vc.dtype == torch.uint8, f"{what}.v_codes: as k_codes")
-    for x in (kp, vp):
-        _need(x.dtype == torch.int32 and tuple(x.shape) == (B, Hk, cap, d // 32), f"{what}: k_par, v_par [B, H_kv, cap, d / 32] int32")
-    for x in cache:
-        _need(x.device == kc.device and x.is_contiguous(), f"{what}: contiguous tensors on one device")
-    return _Kv4CacheC(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, Hk, cap, d)
+    shape = kc.shape
+    dev = kc.get_device()
+    if (len(shape) != 4 or dev < 0 or kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 or vc.shape != shape
+            or shape[3] * 2 not in _DIMS or kp.dtype is not torch.int32 or vp.dtype is not torch.int32
+            or kp.shape != vp.shape or kp.dim() != 4 or kp.shape[:3] != shape[:3] or kp.shape[3] * 16 != shape[3]
+            or kp.get_device() != dev or vc.get_device() != dev or vp.get_device() != dev
+            or not (kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and vp.is_contiguous())):
+        raise ValueError(f"{what}: k_codes, v_codes [B, H_kv, cap, d / 2] uint8 and k_par, v_par [B, H_kv, cap, d / 32] "
+                         "int32, contiguous, on one CUDA device, d 32, 64 or 128")
+    B, Hk, cap, half = shape
+    return _Kv4CacheC(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, Hk, cap, half * 2), dev
 
 
-def _ints(x, n, device, what):
-    _need(x.dtype == torch.int32 and x.dim() == 1 and x.device == device and x.is_contiguous()
-          and (n is None or x.numel() == n), f"{what}: contiguous int32" + ("" if n is None else f" [{n}]") + f" on {device}")
+def _ints(x, n, dev, what):
+    if (x.dtype is not torch.int32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous()
+            or (n is not None and x.shape[0] != n)):
+        raise ValueError(f"{what}: contiguous int32{'' if n is None else f' [{n}]'} on the tensors' device")
 
 
-def _packed(x, like, heads, what):
+def _floats(x, shape, dev, what):
+    if x.dtype is not torch.float32 or tuple(x.shape) != shape or x.get_device() != dev or not x.is_contiguous():
+        raise ValueError(f"{what}: contiguous fp32 {list(shape)} on the cache's device")
+
+
+def _packed(x, heads, N, d, dtype, dev, what):
     # a [heads, N, d] view whose channels are contiguous
-    _need(x.dim() == 3 and (x.stride(2) == 1 or x.shape[2] == 1), f"{what}: [heads, N, d] with contiguous channels")
-    if like is not None:
-        _need(x.dtype == like.dtype and x.device == like.device and x.shape[1:] == like.shape[1:]
-              and (heads is None or x.shape[0] == heads), f"{what}: does not match the other inputs")
+    if (x.dim() != 3 or x.shape[0] != heads or x.shape[1] != N or x.shape[2] != d or x.dtype is not dtype
+            or x.get_device() != dev or x.stride(2) != 1):
+        raise ValueError(f"{what}: [{heads}, {N}, {d}] {dtype} with contiguous channels, on the device of the others")
 
 
 def _strides(*xs):
-    return (ctypes.c_int64 * (2 * len(xs)))(*[s for x in xs for s in x.stride()[:2]])
+    # NULL where all are contiguous
+    for x in xs:
+        if not x.is_contiguous():
+            return (ctypes.c_int64 * (2 * len(xs)))(*[s for y in xs for s in y.stride()[:2]])
+    return None
 
 
 class _On:
     """The device and stream of one call.  With a stream other than the
     current one, what the call allocates comes from that stream's memory, and
     the caching allocator is told of every tensor that both streams touch."""
+    __slots__ = ("ptr", "stream", "current", "guard")
 
-    def __init__(self, device, stream):
-        self.current = torch.cuda.current_stream(device)
-        self.stream = self.current if stream is None else stream
-        self.other = self.stream.cuda_stream != self.current.cuda_stream
-        _need(self.stream.device == device, "stream: of another device than the tensors")
-        self.guard = None
-        if self.other:
-            self.guard = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
+    def __init__(self, dev, stream):
+        self.stream = self.guard = None
+        self.ptr = torch._C._cuda_getCurrentRawStream(dev)
+        if stream is not None:
+            _need(stream.device.index == dev, "stream: of another device than the tensors")
+            if stream.cuda_stream != self.ptr:
+                self.current = torch.cuda.current_stream(dev)
+                self.ptr, self.stream, self.guard = stream.cuda_stream, stream, torch.cuda.stream(stream)
+        if self.guard is None and torch.cuda.current_device() != dev:
+            self.guard = torch.cuda.device(dev)
 
     def __enter__(self):
         if self.guard is not None:
@@ -469,20 +487,16 @@ class _On:
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-    @property
-    def ptr(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
     def uses(self, *given):
         """Tensors of the caller that this call reads or writes."""
-        if self.other:
+        if self.stream is not None:
             for x in given:
                 if x is not None:
                     x.record_stream(self.stream)
 
     def hands(self, *made):
         """Tensors that this call allocated for the caller."""
-        if self.other:
+        if self.stream is not None:
             for x in made:
                 x.record_stream(self.current)
 
@@ -491,19 +505,28 @@ def la_softmax_prefill_workspace_size(H, H_kv, N, d, n_seq) -> int:
     return int(lib().la_softmax_prefill_workspace_size(H, H_kv, N, d, n_seq))
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_ws(B, H, H_kv, cap, d, with_weights):
+    return int(lib().la_kv4_decode_workspace_size(B, H, H_kv, cap, d, with_weights))
+
+
 def la_kv4_decode_workspace_size(B, H, H_kv, cap, d, with_weights=False) -> int:
-    return int(lib().la_kv4_decode_workspace_size(B, H, H_kv, cap, d, int(bool(with_weights))))
+    return _decode_ws(B, H, H_kv, cap, d, int(bool(with_weights)))
 
 
 def la_kv4_evict_workspace_size(B, H_kv, cap, keep) -> int:
     return int(lib().la_kv4_evict_workspace_size(B, H_kv, cap, keep))
 
 
-def _ws(workspace, need, device):
+def _ws(workspace, need, device, dev):
     if workspace is None:
         return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    _need(workspace.device == device and workspace.is_contiguous(), f"workspace: contiguous, on {device}")
+    _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace: contiguous, on the tensors' device")
     return workspace
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
 
 
 def la_softmax_prefill(q, k, v, cu_seqlens, scale=None, out=None, out_dtype=None, workspace=None, stream=None):
@@ -514,28 +537,29 @@ def la_softmax_prefill(q, k, v, cu_seqlens, scale=None, out=None, out_dtype=None
     int32 on the device, sequence s being tokens cu_seqlens[s] ..
     cu_seqlens[s + 1] - 1.  ``scale`` defaults to d ** -0.5.  Returns ``out``
     [H, N, d]; its rows behind the last sequence are left as they were."""
-    _packed(q, None, None, "q")
-    _need(q.is_cuda and q.dtype in _DT, "q: f32, bf16 or f16 on CUDA")
+    _need(q.dim() == 3 and k.dim() == 3 and q.is_cuda and q.dtype in _DT, "q: [H, N, d] f32, bf16 or f16 on CUDA; k: [H_kv, N, d]")
     H, N, d = q.shape
-    _packed(k, q, None, "k")
-    _packed(v, q, k.shape[0], "v")
-    _ints(cu_seqlens, None, q.device, "cu_seqlens")
-    n_seq = cu_seqlens.numel() - 1
+    dev, dt, Hk = q.get_device(), q.dtype, k.shape[0]
+    _packed(q, H, N, d, dt, dev, "q")
+    _packed(k, Hk, N, d, dt, dev, "k")
+    _packed(v, Hk, N, d, dt, dev, "v")
+    _ints(cu_seqlens, None, dev, "cu_seqlens")
+    n_seq = cu_seqlens.shape[0] - 1
     _need(n_seq >= 0, "cu_seqlens: at least one entry")
     if out is not None:
-        _packed(out, None, None, "out")
-        _need(out.shape == q.shape and out.device == q.device and out.dtype in _DT and out_dtype in (None, out.dtype),
-              "out: [H, N, d] on the inputs' device")
-    with _On(q.device, stream) as on:
+        _need(out.dtype in _DT and out_dtype in (None, out.dtype), "out: f32, bf16 or f16")
+        _packed(out, H, N, d, out.dtype, dev, "out")
+    with _On(dev, stream) as on:
         on.uses(q, k, v, cu_seqlens, out, workspace)
         if out is None:
-            out = torch.empty((H, N, d), dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            out = torch.empty((H, N, d), dtype=dt if out_dtype is None else out_dtype, device=q.device)
             on.hands(out)
-        ws = _ws(workspace, 256, q.device)
-        _check("la_softmax_prefill", lib().la_softmax_prefill(
-            _ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], H, k.shape[0], N, d, _ptr(cu_seqlens), n_seq,
-            _strides(q, k, v, out), d ** -0.5 if scale is None else float(scale), _ptr(out), _DT[out.dtype],
-            _ptr(ws), ws.numel() * ws.element_size(), on.ptr))
+        ws = _ws(workspace, 256, q.device, dev)
+        st = lib().la_softmax_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dt], H, Hk, N, d, cu_seqlens.data_ptr(), n_seq,
+            _strides(q, k, v, out), d ** -0.5 if scale is None else scale, out.data_ptr(), _DT[out.dtype],
+            ws.data_ptr(), ws.nbytes, on.ptr)
+    _check("la_softmax_prefill", st)
     return out
 
 
@@ -544,29 +568,29 @@ def la_kv4_append(k, v, cache, start, cu_seqlens=None, stream=None):
     la_softmax_prefill); token t of sequence s goes to position start[s] +
     (t - cu_seqlens[s]); without ``cu_seqlens`` token t is sequence t's only
     one.  Positions outside the cache are dropped.  start: [B] int32."""
-    c = _cache_c(cache)
-    dev = cache.k_codes.device
-    _packed(k, None, None, "k")
-    _packed(v, k, c.H_kv, "v")
-    _need(k.dtype in _DT and k.device == dev and k.shape[0] == c.H_kv and k.shape[2] == c.d,
-          "k, v: [H_kv, N, d] of the cache's heads and head dim, on its device")
+    c, dev = _cache_c(cache)
+    dt = k.dtype
+    _need(k.dim() == 3 and dt in _DT, "k: [H_kv, N, d] f32, bf16 or f16")
+    N = k.shape[1]
+    _packed(k, c.H_kv, N, c.d, dt, dev, "k")
+    _packed(v, c.H_kv, N, c.d, dt, dev, "v")
     _ints(start, c.B, dev, "start")
     if cu_seqlens is not None:
         _ints(cu_seqlens, c.B + 1, dev, "cu_seqlens")
     else:
-        _need(k.shape[1] == c.B, "without cu_seqlens: one token per sequence")
+        _need(N == c.B, "without cu_seqlens: one token per sequence")
     with _On(dev, stream) as on:
         on.uses(k, v, start, cu_seqlens, *cache)
-        _check("la_kv4_append", lib().la_kv4_append(_ptr(k), _ptr(v), _DT[k.dtype], k.shape[1], _strides(k, v),
-                                                    _ptr(cu_seqlens), _ptr(start), ctypes.byref(c), on.ptr))
+        st = lib().la_kv4_append(k.data_ptr(), v.data_ptr(), _DT[dt], N, _strides(k, v), _addr(cu_seqlens),
+                                 start.data_ptr(), c, on.ptr)
+    _check("la_kv4_append", st)
 
 
 def la_kv4_read(cache, start, n_tokens, cu_seqlens=None, out_dtype=torch.float32, stream=None):
     """The cache's values at the positions la_kv4_append would write for the
     same ``start`` and ``cu_seqlens``: (k, v), each [H_kv, n_tokens, d].
     Positions outside the cache and tokens of no sequence give zeros."""
-    c = _cache_c(cache)
-    dev = cache.k_codes.device
+    c, dev = _cache_c(cache)
     _need(out_dtype in _DT and n_tokens >= 0, "out_dtype: f32, bf16 or f16; n_tokens >= 0")
     _ints(start, c.B, dev, "start")
     if cu_seqlens is not None:
@@ -575,11 +599,12 @@ def la_kv4_read(cache, start, n_tokens, cu_seqlens=None, out_dtype=torch.float32
         _need(n_tokens == c.B, "without cu_seqlens: one token per sequence")
     with _On(dev, stream) as on:
         on.uses(start, cu_seqlens, *cache)
-        k = torch.empty((c.H_kv, n_tokens, c.d), dtype=out_dtype, device=dev)
+        k = torch.empty((c.H_kv, n_tokens, c.d), dtype=out_dtype, device=start.device)
         v = torch.empty_like(k)
         on.hands(k, v)
-        _check("la_kv4_read", lib().la_kv4_read(ctypes.byref(c), n_tokens, _ptr(cu_seqlens), _ptr(start), _ptr(k),
-                                                _ptr(v), _DT[out_dtype], on.ptr))
+        st = lib().la_kv4_read(c, n_tokens, _addr(cu_seqlens), start.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               _DT[out_dtype], on.ptr)
+    _check("la_kv4_read", st)
     return k, v
 
 
@@ -591,29 +616,30 @@ def la_kv4_decode(q, cache, lens, scale=None, weights_in=None, weights_out=None,
     receives weights_in (zeros if None; may be the same tensor) plus each
     position's attention weight summed over the head's queries.  Returns
     ``out`` [B, H, d]; a length of 0 gives zeros."""
-    c = _cache_c(cache)
-    dev = cache.k_codes.device
-    _need(q.dim() == 3 and q.is_contiguous() and q.dtype in _DT and q.device == dev and q.shape[0] == c.B
-          and q.shape[2] == c.d, "q: contiguous [B, H, d] of the cache's sequences and head dim, on its device")
-    H = q.shape[1]
-    _ints(lens, c.B, dev, "lens")
-    for x in (weights_in, weights_out):
-        if x is not None:
-            _need(x.dtype == torch.float32 and tuple(x.shape) == (c.B, c.H_kv, c.cap) and x.device == dev
-                  and x.is_contiguous(), "weights: contiguous [B, H_kv, cap] fp32")
+    c, dev = _cache_c(cache)
+    B, Hk, cap, d, dt, shape = c.B, c.H_kv, c.cap, c.d, q.dtype, q.shape
+    if (len(shape) != 3 or shape[0] != B or shape[2] != d or dt not in _DT or q.get_device() != dev
+            or not q.is_contiguous()):
+        raise ValueError("q: contiguous [B, H, d] of the cache's sequences and head dim, on its device")
+    H = shape[1]
+    _ints(lens, B, dev, "lens")
+    if weights_in is not None:
+        _floats(weights_in, (B, Hk, cap), dev, "weights_in")
+    if weights_out is not None:
+        _floats(weights_out, (B, Hk, cap), dev, "weights_out")
     if out is not None:
-        _need(out.shape == q.shape and out.is_contiguous() and out.device == dev and out.dtype in _DT
+        _need(out.shape == shape and out.is_contiguous() and out.get_device() == dev and out.dtype in _DT
               and out_dtype in (None, out.dtype), "out: contiguous [B, H, d] on the cache's device")
     with _On(dev, stream) as on:
         on.uses(q, lens, weights_in, weights_out, out, workspace, *cache)
         if out is None:
-            out = torch.empty((c.B, H, c.d), dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
+            out = torch.empty(shape, dtype=dt if out_dtype is None else out_dtype, device=q.device)
             on.hands(out)
-        ws = _ws(workspace, la_kv4_decode_workspace_size(c.B, H, c.H_kv, c.cap, c.d, weights_out is not None), dev)
-        _check("la_kv4_decode", lib().la_kv4_decode(
-            _ptr(q), _DT[q.dtype], H, ctypes.byref(c), _ptr(lens), c.d ** -0.5 if scale is None else float(scale),
-            _ptr(weights_in), _ptr(weights_out), _ptr(out), _DT[out.dtype], _ptr(ws),
-            ws.numel() * ws.element_size(), on.ptr))
+        ws = _ws(workspace, _decode_ws(B, H, Hk, cap, d, 0 if weights_out is None else 1), q.device, dev)
+        st = lib().la_kv4_decode(
+            q.data_ptr(), _DT[dt], H, c, lens.data_ptr(), d ** -0.5 if scale is None else scale, _addr(weights_in),
+            _addr(weights_out), out.data_ptr(), _DT[out.dtype], ws.data_ptr(), ws.nbytes, on.ptr)
+    _check("la_kv4_decode", st)
     return out
 
 
@@ -626,35 +652,36 @@ def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=Non
     [B, H_kv, keep] int32 (-1 behind them), their weights [B, H_kv, out.cap]
     and the new lengths [B] int32; with ``out`` None (out, kept, out_weights,
     out_lens)."""
-    c = _cache_c(cache)
-    dev = cache.k_codes.device
+    c, dev = _cache_c(cache)
+    B, Hk, cap = c.B, c.H_kv, c.cap
     keep, recent = int(keep), int(recent)
-    _ints(lens, c.B, dev, "lens")
-    _need(weights.dtype == torch.float32 and tuple(weights.shape) == (c.B, c.H_kv, c.cap) and weights.device == dev
-          and weights.is_contiguous(), "weights: contiguous [B, H_kv, cap] fp32")
+    _ints(lens, B, dev, "lens")
+    _floats(weights, (B, Hk, cap), dev, "weights")
     _need(keep >= 1 and 0 <= recent <= keep, "keep >= 1, 0 <= recent <= keep")
+    device = lens.device
+    cap_out = keep
     if out is not None:
-        _need(_cache_c(out, "out").cap >= keep and out.k_codes.device == dev, "out: keep positions at least, on the cache's device")
+        o, dev_o = _cache_c(out, "out")
+        _need(dev_o == dev and o.B == B and o.H_kv == Hk and o.d == c.d and o.cap >= keep,
+              "out: of the cache's sequences, heads and head dim, keep positions at least, on its device")
+        cap_out = o.cap
     if out_weights is not None:
-        cap_out = keep if out is None else out.k_codes.shape[2]
-        _need(out_weights.dtype == torch.float32 and tuple(out_weights.shape) == (c.B, c.H_kv, cap_out)
-              and out_weights.device == dev and out_weights.is_contiguous(),
-              "out_weights: contiguous [B, H_kv, out.cap] fp32")
+        _floats(out_weights, (B, Hk, cap_out), dev, "out_weights")
     with _On(dev, stream) as on:
         on.uses(weights, lens, out_weights, workspace, *cache, *(out or ()))
         dst = out
         if dst is None:
-            dst = KV4Cache.alloc(c.B, c.H_kv, keep, c.d, dev)
+            dst = KV4Cache.alloc(B, Hk, keep, c.d, device)
             on.hands(*dst)
-        o = _cache_c(dst, "out")
+            o, _ = _cache_c(dst, "out")
         if out_weights is None:
-            out_weights = torch.zeros((c.B, c.H_kv, o.cap), dtype=torch.float32, device=dev)
+            out_weights = torch.zeros((B, Hk, cap_out), dtype=torch.float32, device=device)
             on.hands(out_weights)
-        kept = torch.empty((c.B, c.H_kv, keep), dtype=torch.int32, device=dev)
-        out_lens = torch.empty(c.B, dtype=torch.int32, device=dev)
+        kept = torch.empty((B, Hk, keep), dtype=torch.int32, device=device)
+        out_lens = torch.empty(B, dtype=torch.int32, device=device)
         on.hands(kept, out_lens)
-        ws = _ws(workspace, la_kv4_evict_workspace_size(c.B, c.H_kv, c.cap, keep), dev)
-        _check("la_kv4_evict", lib().la_kv4_evict(ctypes.byref(c), _ptr(weights), _ptr(lens), keep, recent,
-                                                  ctypes.byref(o), _ptr(out_weights), _ptr(kept), _ptr(out_lens),
-                                                  _ptr(ws), ws.numel() * ws.element_size(), on.ptr))
+        ws = _ws(workspace, la_kv4_evict_workspace_size(B, Hk, cap, keep), device, dev)
+        st = lib().la_kv4_evict(c, weights.data_ptr(), lens.data_ptr(), keep, recent, o, out_weights.data_ptr(),
+                                kept.data_ptr(), out_lens.data_ptr(), ws.data_ptr(), ws.nbytes, on.ptr)
+    _check("la_kv4_evict", st)
     return (dst, kept, out_weights, out_lens) if out is None else (kept, out_weights, out_lens)

@@ -113,7 +113,7 @@ template <typename InT, typename OutT>
 la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
     LA_BY_D(d, return launch_kernel(softmax_simt_kernel<InT, OutT, D>,
                                     dim3((unsigned)seq_tiles(p.N, p.n_seq, kSsTile), (unsigned)p.H), dim3(kSsThreads),
-                                    softmax_simt_smem<D>(), st, false, "softmax prefill launch", p))
+                                    softmax_simt_smem<D>(), st, true, "softmax prefill launch", p))
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
     const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
@@ -209,12 +209,14 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
         return LA_ERR_INVALID_ARG;
     if (!ws_ok(workspace, workspace_bytes, kWsAlign)) return LA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 2 * sizeof(int), st))) != LA_OK) return s;
     p.q = q; p.k = k; p.v = v; p.out = out; p.cu = cu_seqlens;
     p.H = H; p.group = H / H_kv; p.N = N; p.n_seq = n_seq;
     p.scale_log2 = scale * kLog2e;
-    if (softmax_tc_supported(in_dtype, d))
+    p.status = (int *)workspace;
+    if (softmax_tc_supported(in_dtype, d)) {
+        if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 2 * sizeof(int), st))) != LA_OK) return s;
         return softmax_tc(p, in_dtype, out_dtype, d, (int *)workspace, wait_limit_ns(), st);
+    }
     LA_BY_TYPES(in_dtype, out_dtype, return (run_softmax_simt<InT, OutT>(p, d, st)))
 }
 

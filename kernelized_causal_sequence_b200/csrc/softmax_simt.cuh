@@ -22,6 +22,7 @@ struct SoftmaxParams {
     long q_hs, q_ts, k_hs, k_ts, v_hs, v_ts, o_hs, o_ts;   // strides in elements
     int H, group, N, n_seq;                                // group = H / H_kv
     float scale_log2;                                      // scale * log2(e)
+    int *status;                                           // the workspace's status word (no wait here can give up)
 };
 
 constexpr int kSsTile = 64, kSsThreads = 256, kSsPad = kSsTile + 4;
@@ -76,6 +77,8 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
     float *ks = qs + D * kSsPad;           // [D][kSsPad]
     float *vs = ks + D * kSsPad;           // [64][D]
     float *ps = vs + kSsTile * D;          // [64 keys][kSsPad]
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
     const SeqTile t = seq_tile<kSsTile>(p.cu, p.n_seq, p.N, blockIdx.x);
     if (t.q0 >= t.end) return;
     const int h = blockIdx.y, hk = h / p.group;
