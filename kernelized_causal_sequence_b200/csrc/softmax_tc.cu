@@ -39,7 +39,7 @@ bool map16(CUtensorMap *m, const void *base, la_dtype dt, int heads, int N, int 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename InT, typename OutT, int D, bool PAIR>
+template <typename InT, typename OutT, int D, int MODE>
 la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     const int Hk = sp.H / sp.group;
@@ -49,24 +49,39 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long l
     stc::Params p;
     p.out = sp.out; p.cu = sp.cu; p.o_hs = sp.o_hs; p.o_ts = sp.o_ts;
     p.H = sp.H; p.group = sp.group; p.N = sp.N; p.n_seq = sp.n_seq;
-    p.tiles = seq_tiles(sp.N, sp.n_seq, PAIR ? 128 : 256);
+    p.tiles = seq_tiles(sp.N, sp.n_seq, MODE == stc::kTwoTiles ? 256 : 128);
     p.scale_log2 = sp.scale_log2; p.status = status; p.wait_ns = wait_ns;
-    const long grid = (long)p.tiles * (PAIR ? sp.H / 2 : sp.H);
+    const long grid = (long)p.tiles * (MODE == stc::kTwoHeads ? sp.H / 2 : sp.H);
     if (grid > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
-    return launch_kernel(stc::softmax_tc_kernel<InT, OutT, D, PAIR>, dim3((unsigned)grid), dim3(stc::kThreads),
-                         stc::Cfg<D>::SMEM, st, false, "softmax tensor-core launch", mq, mk, mv, (const InT *)sp.v,
-                         sp.v_hs, sp.v_ts, p);
+    using G = stc::Cfg<D, MODE>;
+    return launch_kernel(stc::softmax_tc_kernel<InT, OutT, D, MODE>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st,
+                         false, "softmax tensor-core launch", mq, mk, mv, (const InT *)sp.v, sp.v_hs, sp.v_ts, p);
+}
+
+// Which slots (us, 16 query heads, one and two slots; S sequences of L tokens):
+//   d 128, heads shared evenly: two heads read each key/value tile once for
+//     both (16 x 1000: 133 / 119; 1 x 8192: 288 / 246; 64 x 200: 84 / 78)
+//   d 128, else: two tiles of one head, but for short sequences, which leave
+//     the second empty (256 x 64: 139 / 212; 64 x 256: 93 / 96; 32 x 512: 108 / 105)
+//   d 64: the tiles are half as large and the exponentials bound it; two CTAs
+//     of one slot overlap each other's start and end (16 x 1000: 99 / 112;
+//     1 x 8192: 226 / 233), but for long sequences with heads shared evenly
+//     (16 x 1000: 98 / 100; 4 x 4096: 242 / 237)
+template <typename InT, typename OutT, int D>
+la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
+    const bool even = sp.group % 2 == 0;
+    if constexpr (D == 128) {
+        if (even) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
+        if ((long)sp.N > 384L * sp.n_seq) return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, status, wait_ns, st);
+    } else {
+        if (even && (long)sp.N > 2048L * sp.n_seq) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
+    }
+    return run<InT, OutT, D, stc::kOneTile>(sp, dt, status, wait_ns, st);
 }
 
 template <typename InT, typename OutT>
 la_status by_shape(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
-    const bool pair = sp.group % 2 == 0;
-    if (d == 128) {
-        if (pair) return run<InT, OutT, 128, true>(sp, dt, status, wait_ns, st);
-        return run<InT, OutT, 128, false>(sp, dt, status, wait_ns, st);
-    }
-    if (pair) return run<InT, OutT, 64, true>(sp, dt, status, wait_ns, st);
-    return run<InT, OutT, 64, false>(sp, dt, status, wait_ns, st);
+    return d == 128 ? by_slots<InT, OutT, 128>(sp, dt, status, wait_ns, st) : by_slots<InT, OutT, 64>(sp, dt, status, wait_ns, st);
 }
 
 }  // namespace

@@ -51,18 +51,24 @@ namespace stc {
 
 using namespace tc;
 
-constexpr int kThreads = 352;
 constexpr int kBlock = 128;   // keys of a block, rows of a slot
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScrubWarp = 10;
+
+// What the slots of a CTA are: one tile of queries (two CTAs per SM), two
+// consecutive tiles of one head, or the same tile of two heads.
+enum Slots { kOneTile = 0, kTwoTiles = 1, kTwoHeads = 2 };
 constexpr float kLazyLog2 = 8.f;   // how far (log2) the maximum may outgrow the reference
 
-template <int D> struct Cfg {
+template <int D, int MODE> struct Cfg {
+    static constexpr int SLOTS = MODE == kOneTile ? 1 : 2;
+    static constexpr int THREADS = SLOTS == 1 ? 256 : 352;
+    static constexpr int TMA_WARP = 4 * SLOTS, MMA_WARP = TMA_WARP + 1, SCRUB_WARP = TMA_WARP + 2;
     static constexpr int KB = D / 64;                  // 128-byte boxes per row
     static constexpr int BOXB = kBlock * 128;
     static constexpr int TILE = kBlock * D * 2;
-    static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in flight (all the shared memory there is)
+    // K and V tiles in flight: all the shared memory there is
+    static constexpr int NST = SLOTS == 1 ? (D == 128 ? 2 : 5) : (D == 128 ? 5 : 8);
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_KV = SLOTS * TILE;
     static constexpr int OFF_BAR = OFF_KV + NST * TILE;
     static constexpr int B_Q = 0, B_KV_FULL = 2, B_KV_EMPTY = B_KV_FULL + NST, B_S = B_KV_EMPTY + NST;
     static constexpr int B_P = B_S + 2, B_O = B_P + 2, B_CLEAN = B_O + 2;
@@ -74,8 +80,9 @@ template <int D> struct Cfg {
     static constexpr int OFF_ABORT = OFF_TMEM + 4;
     static constexpr int OFF_FLAG = OFF_ABORT + 4;     // two ints: a diagonal block held NaN or infinities
     static constexpr int SMEM = OFF_FLAG + 8 + 1024;   // + alignment
-    static constexpr int T_S = 0, T_O = 256;           // TMEM: S / P of slot s at 128 s, O at 256 + 128 s
-    static_assert(SMEM <= 232448, "shared memory");
+    // TMEM: S / P of slot s at 128 s, O behind them (two CTAs of one slot each share the 512 columns)
+    static constexpr int T_S = 0, T_O = 128 * SLOTS, TMEM_COLS = 256 * SLOTS;
+    static_assert(SMEM <= (SLOTS == 1 ? 115712 : 232448), "shared memory");
 };
 
 struct Params {
@@ -129,8 +136,8 @@ template <typename InT> __device__ __forceinline__ uint32_t finite_or_zero2(uint
 // A diagonal block's value tile [KB boxes][128 rows][128 B]: rows at or past n
 // are zeroed, NaN and infinities become 0 (returns whether there were any).
 // One warp.
-template <typename InT, int D> __device__ __noinline__ bool scrub_values(uint8_t *tile, int n, int lane) {
-    constexpr int CH = Cfg<D>::TILE / 16;   // 16-byte chunks; chunk i of box b, row r: b * 1024 + r * 8 + i
+template <typename InT, int TILE> __device__ __forceinline__ bool scrub_values(uint8_t *tile, int n, int lane) {
+    constexpr int CH = TILE / 16;   // 16-byte chunks; chunk i of box b, row r: b * 1024 + r * 8 + i
     uint32_t acc = 0u;
 #pragma unroll 8
     for (int i = lane; i < CH; i += 32) {
@@ -161,7 +168,7 @@ template <typename InT, int D> __device__ __noinline__ bool scrub_values(uint8_t
 // Adds the NaN and infinities of values j0 .. min(j1, row) to this thread's
 // row of O (p > 0 times infinity is infinity).  Rare; whole warp.
 template <typename InT, int D>
-__device__ __noinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long ts, int j0, int j1, int row) {
+__device__ __forceinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long ts, int j0, int j1, int row) {
     for (int cb = 0; cb < D / 32; ++cb) {
         uint32_t u[32];
         tmem_ld32(t_o + cb * 32, u);
@@ -178,12 +185,29 @@ __device__ __noinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long 
     tmem_st_wait();
 }
 
-template <typename InT, typename OutT, int D, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+// mbar_wait without a call: a kernel that redistributes its registers may not
+// call functions.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const AbortCtx &ab, int code) {
+    const uint32_t hint = ab.hint();
+    if (mbar_try_wait(bar, parity, hint)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity, hint)) {
+        if (*ab.flag) return false;
+        if (globaltimer_ns() - t0 >= ab.limit_ns) {
+            raise_abort(ab, code);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <typename InT, typename OutT, int D, int MODE>
+__global__ void __launch_bounds__(Cfg<D, MODE>::THREADS, MODE == kOneTile ? 2 : 1)
 softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const InT *__restrict__ v_gmem, long v_hs, long v_ts,
                   const Params p) {
-    using G = Cfg<D>;
+    using G = Cfg<D, MODE>;
+    constexpr bool PAIR = MODE == kTwoHeads;
     extern __shared__ uint8_t stc_smem_raw[];
     uint8_t *smem = stc_smem_raw + ((1024u - (smem_u32(stc_smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + G::OFF_BAR);
@@ -196,12 +220,12 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // which have the most keys, first
     const int nhp = PAIR ? p.H / 2 : p.H;
     const int hp = blockIdx.x % nhp, tile = p.tiles - 1 - blockIdx.x / nhp;
-    const SeqTile t = seq_tile<PAIR ? 128 : 256>(p.cu, p.n_seq, p.N, tile);
+    const SeqTile t = seq_tile<MODE == kTwoTiles ? 256 : 128>(p.cu, p.n_seq, p.N, tile);
     if (t.q0 >= t.end) return;
     const int h0 = PAIR ? 2 * hp : hp, hk = h0 / p.group;
     // blocks of each slot; the last is the diagonal one
     const int n0 = (t.q0 - t.begin) / kBlock + 1;
-    const int n1 = PAIR ? n0 : (t.q0 + kBlock < t.end ? n0 + 1 : 0);
+    const int n1 = PAIR ? n0 : MODE == kTwoTiles && t.q0 + kBlock < t.end ? n0 + 1 : 0;
     const int nb = max(n0, n1);
     const int n_diag = n1 > n0 ? 2 : 1;   // diagonal blocks: n0 - 1 and, with two row tiles, n0
 
@@ -212,8 +236,8 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int i = 0; i < G::NBAR; ++i) mbar_init(&bar[i], (i == G::B_P || i == G::B_P + 1) ? 4 : 1);
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tmem_alloc(tmem_addr, 512);
-    if (warp == kTmaWarp && lane == 0) {
+    if (warp == G::MMA_WARP) tmem_alloc(tmem_addr, G::TMEM_COLS);
+    if (warp == G::TMA_WARP && lane == 0) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
@@ -222,8 +246,12 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_addr;
-
-    if (warp == kTmaWarp) {
+    // One slot: the softmax warps need more registers than the 128 that two
+    // CTAs of 256 threads leave each; 128 x 200 + 128 x 56 is what there is.
+    // (Two slots: 352 threads have 168, which is enough.)
+    if (warp >= G::TMA_WARP) {
+    if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == G::TMA_WARP) {
         if (lane == 0) {
             int issued = 0;
             for (int s = 0; s < 2; ++s) {
@@ -242,7 +270,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             for (int i = 1; i < 2 * nb; ++i) {
                 const int st = i % G::NST, use = i / G::NST;
-                if (use > 0 && !mbar_wait(&bar[G::B_KV_EMPTY + st], (use - 1) & 1, ab, 1)) break;
+                if (use > 0 && !wait_bar(&bar[G::B_KV_EMPTY + st], (use - 1) & 1, ab, 1)) break;
                 const int dg = (i >> 1) - (n0 - 1);
                 uint64_t *full = &bar[(i & 1) && dg >= 0 ? G::B_VD + dg : G::B_KV_FULL + st];
                 mbar_expect_tx(full, G::TILE);
@@ -255,21 +283,21 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             // for by its reader too, unless that gave up)
             volatile int never = 0;
             AbortCtx timed{&never, nullptr, kDrainLimitNs};
-            mbar_wait(&bar[G::B_Q], 0, timed, 0);
-            if (n1 > 0) mbar_wait(&bar[G::B_Q + 1], 0, timed, 0);
+            wait_bar(&bar[G::B_Q], 0, timed, 0);
+            if (n1 > 0) wait_bar(&bar[G::B_Q + 1], 0, timed, 0);
             for (int i = max(0, issued - G::NST); i < issued; ++i) {
                 const int dg = (i >> 1) - (n0 - 1);
-                if ((i & 1) && dg >= 0) mbar_wait(&bar[G::B_VD + dg], 0, timed, 0);
-                else mbar_wait(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, timed, 0);
+                if ((i & 1) && dg >= 0) wait_bar(&bar[G::B_VD + dg], 0, timed, 0);
+                else wait_bar(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, timed, 0);
             }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == G::MMA_WARP) {
         if (lane == 0) {
             constexpr bool BF = std::is_same<InT, bf16>::value;
             constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
             constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
             const uint32_t sb = smem_u32(smem);
-            auto full = [&](int i) { return mbar_wait(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, ab, 2); };
+            auto full = [&](int i) { return wait_bar(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, ab, 2); };
             auto product_s = [&](int s, int j) {
                 const uint64_t a = sdesc_sw128(sb + G::OFF_Q + s * G::TILE, 16, 1024);
                 const uint64_t b = sdesc_sw128(sb + G::OFF_KV + (2 * j % G::NST) * G::TILE, 16, 1024);
@@ -283,7 +311,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             bool ok = full(0);
             for (int s = 0; s < 2 && ok; ++s) {
                 if (s == 1 && n1 == 0) continue;
-                ok = mbar_wait(&bar[G::B_Q + s], 0, ab, 3);
+                ok = wait_bar(&bar[G::B_Q + s], 0, ab, 3);
                 if (!ok) break;
                 tc_fence_after();
                 product_s(s, 0);
@@ -294,15 +322,16 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int s = 0; s < 2 && ok; ++s) {
                     const int n = s ? n1 : n0;
                     if (j >= n) continue;
-                    ok = (j < n0 - 1 ? full(2 * j + 1) : mbar_wait(&bar[G::B_CLEAN + j - (n0 - 1)], 0, ab, 4)) &&
-                         mbar_wait(&bar[G::B_P + s], j & 1, ab, 5);
+                    ok = (j < n0 - 1 ? full(2 * j + 1) : wait_bar(&bar[G::B_CLEAN + j - (n0 - 1)], 0, ab, 4)) &&
+                         wait_bar(&bar[G::B_P + s], j & 1, ab, 5);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t bv = sdesc_sw128(sb + G::OFF_KV + st_v * G::TILE, G::BOXB, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < kBlock / 16; ++kk)
+                    for (int kk = 0; kk < kBlock / 16; ++kk) {
                         mma_ts(tmem + G::T_O + 128 * s, tmem + G::T_S + 128 * s + kk * 8,
                                bv + (uint64_t)((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                    }
                     if (j == n - 1) mma_commit(&bar[G::B_O + s]);
                     if (j + 1 < n) {
                         ok = full(2 * j + 2);
@@ -318,19 +347,21 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             volatile int never = 0;
             AbortCtx timed{&never, nullptr, kDrainLimitNs};
             mma_commit(&bar[G::B_DRAIN]);
-            mbar_wait(&bar[G::B_DRAIN], 0, timed, 0);
+            wait_bar(&bar[G::B_DRAIN], 0, timed, 0);
         }
-    } else if (warp == kScrubWarp) {
+    } else if (warp == G::SCRUB_WARP) {
         for (int b = 0; b < n_diag; ++b) {
             const int j = n0 - 1 + b, i = 2 * j + 1;
-            if (!mbar_wait(&bar[G::B_VD + b], 0, ab, 6)) break;
+            if (!wait_bar(&bar[G::B_VD + b], 0, ab, 6)) break;
             const int n = t.end - (t.begin + j * kBlock);   // rows of the sequence
-            if (scrub_values<InT, D>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane) && lane == 0) flag[b] = 1;
+            if (scrub_values<InT, G::TILE>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane) && lane == 0) flag[b] = 1;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[G::B_CLEAN + b]);
         }
+    }
     } else {
+        if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // softmax of slot s: thread = row
         const int s = warp >> 2, q = warp & 3;
         const int n = s ? n1 : n0;
@@ -342,7 +373,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            ok = mbar_wait(&bar[G::B_S + s], j & 1, ab, 7);
+            ok = wait_bar(&bar[G::B_S + s], j & 1, ab, 7);
             if (!ok) break;
             tc_fence_after();
             uint32_t u[4][32];
@@ -407,7 +438,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             unpack2(sum[1], s2, s3);
             l += (s0 + s1) + (s2 + s3);
         }
-        if (ok && n > 0) ok = mbar_wait(&bar[G::B_O + s], 0, ab, 8);
+        if (ok && n > 0) ok = wait_bar(&bar[G::B_O + s], 0, ab, 8);
         if (ok && n > 0) {
             tc_fence_after();
             const int row = q0 + r;
@@ -464,9 +495,9 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == G::MMA_WARP) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, G::TMEM_COLS);
     }
 }
 

@@ -157,6 +157,12 @@ PREFILL = [
     (torch.float16, None, 64, 8, 1, [1, 300, 0, 0, 511], 0),
     (torch.float16, torch.float32, 128, 2, 2, [1000, 24], 0),
     (torch.float16, None, 128, 3, 1, [2049], 1),
+    # each way the tensor-core kernel fills a CTA, at d 64 and 128: two heads, two tiles, one tile
+    (torch.bfloat16, None, 64, 4, 2, [2500, 2100], 1),
+    (torch.float16, torch.float32, 64, 2, 1, [2305], 0),
+    (torch.bfloat16, None, 128, 3, 3, [1, 130, 77, 0, 256, 383, 300], 65),
+    (torch.float16, torch.float32, 128, 1, 1, [255, 129, 128, 1], 0),
+    (torch.bfloat16, torch.float32, 128, 3, 1, [700, 384, 900], 3),
 ]
 
 
@@ -206,21 +212,34 @@ def test_prefill_many_single_tokens(la, dtype, d):
 def test_prefill_hidden_keys_do_not_reach(la, dtype, d, bad):
     """A NaN or infinity in a key or value leaves the queries before it, the
     other channels and the other sequences exactly as they are without it."""
-    lens = [300, 150]
-    q, k, v = prefill_inputs(dtype, d, 4, 2, 450, seed=3)
+    hidden_keys(la, dtype, d, 4, 2, bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,first", [(3, 3, 300), (3, 3, 900), (4, 2, 5000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_hidden_keys_all_slots(la, H, Hkv, first, d):
+    """The same where a CTA holds one tile, two tiles and two heads."""
+    hidden_keys(la, torch.bfloat16, d, H, Hkv, math.nan, first=first)
+
+
+def hidden_keys(la, dtype, d, H, Hkv, bad, first=300):
+    lens = [first, 150]
+    G = H // Hkv
+    q, k, v = prefill_inputs(dtype, d, H, Hkv, first + 150, seed=3)
     run = lambda kk, vv: la.la_softmax_prefill(q.to(DEV), kk.to(DEV), vv.to(DEV), cu_of(lens)).cpu()
     clean = run(k, v)
-    for at in (5, 131, 299):
+    for at in (5, 131, first - 1):
         kb, vb = k.clone(), v.clone()
         vb[0, at, 3] = bad
         got = run(k, vb)
         same = torch.ones_like(clean, dtype=torch.bool)
-        same[:2, at:300, 3] = False
+        same[:G, at:first, 3] = False
         assert torch.equal(got[same], clean[same])
-        assert not torch.isfinite(got[:2, at:300, 3]).any()
+        assert not torch.isfinite(got[:G, at:first, 3]).any()
         kb[0, at, 3] = bad
         got = run(kb, v)
-        same[:2, at:300] = False
+        same[:G, at:first] = False
         assert torch.equal(got[same], clean[same])
 
 
