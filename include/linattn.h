@@ -455,7 +455,8 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
                        int recent, const la_kv4_cache *out, float *out_weights, int32_t *kept,
                        int32_t *out_lens, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace la_kv4_evict needs (0 for sizes it refuses). */
+/* Bytes of workspace la_kv4_evict needs where kept is NULL (with it: none; 0
+ * for sizes it refuses). */
 size_t la_kv4_evict_workspace_size(int B, int H_kv, int cap, int keep);
 
 /*

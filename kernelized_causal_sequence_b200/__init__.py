@@ -643,7 +643,7 @@ def la_kv4_decode(q, cache, lens, scale=None, weights_in=None, weights_out=None,
     return out
 
 
-def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=None, workspace=None, stream=None):
+def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=None, stream=None):
     """Cuts every (sequence, head) down to ``keep`` positions: the ``recent``
     newest and the heaviest of the others (ties to the lower position), moved
     in their order to the front of ``out``, another cache of at least ``keep``
@@ -668,7 +668,7 @@ def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=Non
     if out_weights is not None:
         _floats(out_weights, (B, Hk, cap_out), dev, "out_weights")
     with _On(dev, stream) as on:
-        on.uses(weights, lens, out_weights, workspace, *cache, *(out or ()))
+        on.uses(weights, lens, out_weights, *cache, *(out or ()))
         dst = out
         if dst is None:
             dst = KV4Cache.alloc(B, Hk, keep, c.d, device)
@@ -680,8 +680,8 @@ def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=Non
         kept = torch.empty((B, Hk, keep), dtype=torch.int32, device=device)
         out_lens = torch.empty(B, dtype=torch.int32, device=device)
         on.hands(kept, out_lens)
-        ws = _ws(workspace, la_kv4_evict_workspace_size(B, Hk, cap, keep), device, dev)
+        # (with `kept` the library needs no workspace)
         st = lib().la_kv4_evict(c, weights.data_ptr(), lens.data_ptr(), keep, recent, o, out_weights.data_ptr(),
-                                kept.data_ptr(), out_lens.data_ptr(), ws.data_ptr(), ws.nbytes, on.ptr)
+                                kept.data_ptr(), out_lens.data_ptr(), None, 0, on.ptr)
     _check("la_kv4_evict", st)
     return (dst, kept, out_weights, out_lens) if out is None else (kept, out_weights, out_lens)

@@ -175,7 +175,7 @@ template <int D> struct DecCfg {
 };
 template <int D> constexpr size_t kv4_decode_smem(int nt) {
     const size_t ring = (size_t)kDecWarps * DecCfg<D>::WARP;
-    const size_t join = (size_t)kDecWarps * 8 * nt * (D + 2) * sizeof(float);
+    const size_t join = (size_t)kDecWarps * 8 * nt * (D + 2) * sizeof(float) + 8 * nt * sizeof(float);
     return ring > join ? ring : join;
 }
 
@@ -581,6 +581,7 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
     // ---- join the warps: [warp][head][D], then [warp][head] (m, l)
     float *jo = reinterpret_cast<float *>(dec_smem);
     float2 *jml = reinterpret_cast<float2 *>(jo + kDecWarps * HB * D);
+    float *jlse = reinterpret_cast<float *>(jml + kDecWarps * HB);   // [head]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float bs[G], ls = l[nt];
@@ -622,13 +623,24 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
         if (slot < 0) {
             const float inv = 1.f / L;
             store4<OutT>((OutT *)p.out + (h0 + col) * D + c4 * 4, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-            if (p.row_ml && c4 == 0) p.row_ml[h0 + col] = make_float2(M_, L);
+            if (p.row_ml && c4 == 0) {
+                p.row_ml[h0 + col] = make_float2(M_, L);
+                jlse[col] = M_ + log2f(L);
+            }
         } else {
             *reinterpret_cast<float4 *>(p.part_o + ((long)slot * HB + col) * D + c4 * 4) = a;
             if (c4 == 0) p.part_ml[slot * HB + col] = make_float2(M_, L);
         }
     }
     __syncthreads();   // the next row's rings take this memory again
+    // weights where this CTA has the whole group's row (else: kv4_finish_kernel)
+    if (p.weights_out && p.whole && p.head_blocks == 1) {
+        for (int t = threadIdx.x; t < n; t += kDecWarps * 32) {
+            float sum = 0.f;
+            for (int i = 0; i < heads; ++i) sum += ex2_approx(p.scores[(h0 + i) * p.c.cap + t] - jlse[i]);
+            p.weights_out[row0 + t] = (p.weights_in ? p.weights_in[row0 + t] : 0.f) + sum;
+        }
+    }
 }
 
 template <typename InT, typename OutT, int D, int NT>

@@ -25,7 +25,7 @@ struct Kv4EvictParams {
     int keep, recent;
     float *out_weights;
     int32_t *kept, *out_lens;
-    int32_t *list;       // [B, Hkv, keep] workspace
+    int32_t *list;       // [B, Hkv, keep]: kept, or the workspace
 };
 
 constexpr int kEvictMaxCluster = 8, kEvictKeys = 8;   // CTAs of a cluster, keys of a thread
@@ -96,7 +96,7 @@ template <int D, int THREADS> __global__ void __launch_bounds__(THREADS) kv4_evi
     const long bh = bh_i;
     const int n = min(max(p.lens[b], 0), p.c.cap);
     const float *w = p.weights + bh * p.c.cap;
-    int32_t *list = p.list + bh * p.keep, *kept_out = p.kept ? p.kept + bh * p.keep : nullptr;
+    int32_t *list = p.list + bh * p.keep;
     const int kept = min(n, p.keep);
     // positions below `old` compete, the others stay
     const int old = n <= p.keep ? 0 : n - p.recent;
@@ -230,7 +230,6 @@ template <int D, int THREADS> __global__ void __launch_bounds__(THREADS) kv4_evi
                 const int at = s0 + s * SPAN + i * THREADS + tid;
                 const uint32_t to = at_run + sh.cells[i * NW + warp] + __popc(tm[i] & ((1u << lane) - 1));
                 list[to] = at;
-                if (kept_out) kept_out[to] = at;
             }
         eq_run += eqs;
         at_run += tks;
@@ -238,8 +237,8 @@ template <int D, int THREADS> __global__ void __launch_bounds__(THREADS) kv4_evi
     }
     if (rank == 0) {
         if (p.out_lens && bh_i % p.c.Hkv == 0 && tid == 0) p.out_lens[b] = kept;
-        if (kept_out)
-            for (int i = kept + tid; i < p.keep; i += THREADS) kept_out[i] = -1;
+        if (p.kept)
+            for (int i = kept + tid; i < p.keep; i += THREADS) list[i] = -1;
     }
     // the rows of this CTA's part of the list; eight threads a row, four rows in flight each
     const int r = tid & 7, end = (int)at_run;

@@ -109,11 +109,17 @@ inline unsigned stride_grid(long items, int per, long others) {
     if (out == LA_F16) { using InT = f16; using OutT = f16; CALL; }                         \
     { using InT = f16; using OutT = float; CALL; }
 
+template <typename InT, typename OutT, int BM>
+la_status run_softmax_simt_bm(const SoftmaxParams &p, int d, cudaStream_t st) {
+    LA_BY_D(d, return launch_kernel(softmax_simt_kernel<InT, OutT, D, BM>,
+                                    dim3((unsigned)seq_tiles(p.N, p.n_seq, BM), (unsigned)p.H), dim3(kSsThreads),
+                                    softmax_simt_smem<D, BM>(), st, true, "softmax prefill launch", p))
+}
 template <typename InT, typename OutT>
 la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
-    LA_BY_D(d, return launch_kernel(softmax_simt_kernel<InT, OutT, D>,
-                                    dim3((unsigned)seq_tiles(p.N, p.n_seq, kSsTile), (unsigned)p.H), dim3(kSsThreads),
-                                    softmax_simt_smem<D>(), st, true, "softmax prefill launch", p))
+    // tiles of 64 queries fill the machine, or tiles of 16 for more CTAs
+    if ((long)seq_tiles(p.N, p.n_seq, 64) * p.H >= kNumSMs) return run_softmax_simt_bm<InT, OutT, 64>(p, d, st);
+    return run_softmax_simt_bm<InT, OutT, 16>(p, d, st);
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
     const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
@@ -156,7 +162,7 @@ template <typename InT, typename OutT, int D, int NT>
 la_status run_decode_nt(const Kv4DecodeParams &p, cudaStream_t st) {
     la_status s = launch_kernel(kv4_decode_kernel<InT, OutT, D, NT>, dim3((unsigned)p.n_cta), dim3(kDecWarps * 32),
                                 kv4_decode_smem<D>(NT), st, true, "kv4 decode launch", p);
-    if (s != LA_OK || (p.whole && !p.weights_out)) return s;
+    if (s != LA_OK || (p.whole && (!p.weights_out || p.head_blocks == 1))) return s;
     const unsigned ob = p.whole ? 0u : (unsigned)p.group;
     // (four positions a thread, at most four blocks per SM)
     const unsigned wb = p.weights_out ? stride_grid(p.c.cap, 4 * kFinThreads, 2L * p.c.Hkv * p.c.B) : 0u;
@@ -322,13 +328,14 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     if (overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), out_weights,
                 (size_t)out->B * out->H_kv * out->cap * sizeof(float)))
         return LA_ERR_INVALID_ARG;
-    const size_t need = ws_up((size_t)cache->B * cache->H_kv * keep * sizeof(int32_t));
+    // the list of kept positions: the caller's `kept`, or the workspace
+    const size_t need = kept ? 0 : ws_up((size_t)cache->B * cache->H_kv * keep * sizeof(int32_t));
     if (!ws_ok(workspace, workspace_bytes, need)) return LA_ERR_INVALID_ARG;
     Kv4EvictParams p;
     std::memset(&p, 0, sizeof(p));
     p.c = dev_cache(cache); p.o = dev_cache(out); p.weights = weights; p.lens = lens; p.keep = keep;
     p.recent = recent; p.out_weights = out_weights; p.kept = kept; p.out_lens = out_lens;
-    p.list = (int32_t *)workspace;
+    p.list = kept ? kept : (int32_t *)workspace;
     cudaStream_t st = (cudaStream_t)stream;
     // short caches: small blocks, whose barriers are cheaper; long ones: as many CTAs
     // of a (sequence, head) as its positions fill with 8 keys a thread and the

@@ -2,13 +2,15 @@
 // CUDA cores: fp32 inputs (whose 1e-4 class the 16-bit tensor-core operands
 // cannot meet) and head dim 32.
 //
-// One CTA takes 64 queries of one head and walks the keys up to its last
-// query in tiles of 64, keeping for each row the running maximum m, the sum l
-// and the unnormalised output o (all fp32):
+// One CTA takes BM queries of one head (64, or 16 where 64 would leave most SMs
+// without work) and walks the keys up to its last query in tiles of 64, keeping
+// for each row the running maximum m, the sum l and the unnormalised output o
+// (all fp32):
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),
 //   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = scale log2(e) q.k_j.
-// 256 threads as 16 x 16; a thread owns 4 rows x 4 keys of the scores and
-// 4 rows x D/16 channels of the output.
+// 256 threads as 16 x 16; a thread owns BM/16 rows x 4 keys of the scores and
+// BM/16 rows x D/16 channels of the output.  The next tile's keys and values
+// travel to registers while a tile is computed.
 #pragma once
 #include "common.cuh"
 #include "packed.cuh"
@@ -26,8 +28,8 @@ struct SoftmaxParams {
 };
 
 constexpr int kSsTile = 64, kSsThreads = 256, kSsPad = kSsTile + 4;
-template <int D> constexpr size_t softmax_simt_smem() {
-    return sizeof(float) * (2 * D * kSsPad + kSsTile * D + kSsTile * kSsPad);
+template <int D, int BM> constexpr size_t softmax_simt_smem() {
+    return sizeof(float) * (D * (BM + 4) + D * kSsPad + kSsTile * D + kSsTile * (BM + 4));
 }
 
 template <typename T> __device__ __forceinline__ float4 load4(const T *p);
@@ -50,77 +52,100 @@ template <> __device__ __forceinline__ void store4<float>(float *p, float a, flo
     *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
 }
 
-// rows [r0, r0 + 64) of a [T][D] matrix to shared memory, rows at or past end as zeros;
-// TRANS: [D][kSsPad] (channel-major), else [64][D]
-template <typename T, int D, bool TRANS>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, long ts, int r0, int end) {
-    for (int i = threadIdx.x; i < kSsTile * (D / 4); i += kSsThreads) {
-        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < end) x = load4<T>(src + (long)(r0 + r) * ts + c);
-        if (TRANS) {
-            dst[(c + 0) * kSsPad + r] = x.x;
-            dst[(c + 1) * kSsPad + r] = x.y;
-            dst[(c + 2) * kSsPad + r] = x.z;
-            dst[(c + 3) * kSsPad + r] = x.w;
-        } else {
-            *reinterpret_cast<float4 *>(dst + r * D + c) = x;
-        }
+template <int N> __device__ __forceinline__ void lds_rows(const float *p, float (&x)[N]) {
+    if constexpr (N == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+        x[0] = p[0];
     }
 }
 
-template <typename InT, typename OutT, int D>
+template <typename InT, typename OutT, int D, int BM>
 __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams p) {
-    constexpr int CT = D / 16;   // output channels per thread
+    constexpr int CT = D / 16;                           // output channels per thread
+    constexpr int RW = BM / 16;                          // rows per thread
+    constexpr int QP = BM + 4;                           // row pitch of the channel-major queries and of P
+    constexpr int NL = kSsTile * (D / 4) / kSsThreads;   // 4-channel pieces of a tile per thread
     extern __shared__ __align__(16) float ss_smem[];
-    float *qs = ss_smem;                   // [D][kSsPad]
-    float *ks = qs + D * kSsPad;           // [D][kSsPad]
+    float *qs = ss_smem;                   // [D][QP]
+    float *ks = qs + D * QP;               // [D][kSsPad]
     float *vs = ks + D * kSsPad;           // [64][D]
-    float *ps = vs + kSsTile * D;          // [64 keys][kSsPad]
+    float *ps = vs + kSsTile * D;          // [64 keys][QP]
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
-    const SeqTile t = seq_tile<kSsTile>(p.cu, p.n_seq, p.N, blockIdx.x);
+    const SeqTile t = seq_tile<BM>(p.cu, p.n_seq, p.N, blockIdx.x);
     if (t.q0 >= t.end) return;
     const int h = blockIdx.y, hk = h / p.group;
     const InT *Q = (const InT *)p.q + h * p.q_hs;
     const InT *K = (const InT *)p.k + hk * p.k_hs;
     const InT *V = (const InT *)p.v + hk * p.v_hs;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_tile<InT, D, true>(qs, Q, p.q_ts, t.q0, t.end);
-    float m[4], l[4], o[4][CT];
+    const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+    // keys: thread = row (conflict-free transposed stores); values: thread = piece of a row
+    float4 kr[NL], vr[NL];
+    auto load = [&](int j0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NL; ++i) {
+            const int kj = j0 + tid % kSsTile, kc = (tid / kSsTile + i * (kSsThreads / kSsTile)) * 4;
+            const int x = tid + i * kSsThreads, vj = j0 + x / (D / 4), vc = (x % (D / 4)) * 4;
+            kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (kj < t.end) kr[i] = load4<InT>(K + (long)kj * p.k_ts + kc);
+            if (vj < t.end) vr[i] = load4<InT>(V + (long)vj * p.v_ts + vc);
+        }
+    };
+    load(t.begin);
+    for (int x = tid; x < BM * (D / 4); x += kSsThreads) {
+        const int r = x % BM, c = (x / BM) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t.q0 + r < t.end) v = load4<InT>(Q + (long)(t.q0 + r) * p.q_ts + c);
+        qs[(c + 0) * QP + r] = v.x;
+        qs[(c + 1) * QP + r] = v.y;
+        qs[(c + 2) * QP + r] = v.z;
+        qs[(c + 3) * QP + r] = v.w;
+    }
+    float m[RW], l[RW], o[RW][CT];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) o[i][c] = 0.f;
     }
-    const int last = min(t.q0 + kSsTile, t.end);   // keys [begin, last)
+    const int last = min(t.q0 + BM, t.end);   // keys [begin, last)
     for (int j0 = t.begin; j0 < last; j0 += kSsTile) {
         __syncthreads();
-        load_tile<InT, D, true>(ks, K, p.k_ts, j0, t.end);
-        load_tile<InT, D, false>(vs, V, p.v_ts, j0, t.end);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int r = tid % kSsTile, kc = (tid / kSsTile + i * (kSsThreads / kSsTile)) * 4, x = tid + i * kSsThreads;
+            ks[(kc + 0) * kSsPad + r] = kr[i].x;
+            ks[(kc + 1) * kSsPad + r] = kr[i].y;
+            ks[(kc + 2) * kSsPad + r] = kr[i].z;
+            ks[(kc + 3) * kSsPad + r] = kr[i].w;
+            *reinterpret_cast<float4 *>(vs + x * 4) = vr[i];
+        }
         __syncthreads();
-        float s[4][4] = {};
+        if (j0 + kSsTile < last) load(j0 + kSsTile);
+        float s[RW][4] = {};
 #pragma unroll 8
         for (int c = 0; c < D; ++c) {
-            const float4 a4 = *reinterpret_cast<const float4 *>(qs + c * kSsPad + ty * 4);
-            const float4 b4 = *reinterpret_cast<const float4 *>(ks + c * kSsPad + tx * 4);
-            const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+            float a[RW], b[4];
+            lds_rows(qs + c * QP + ty * RW, a);
+            lds_rows(ks + c * kSsPad + tx * 4, b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < RW; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][j] = fmaf(a[i], b[j], s[i][j]);
         }
         const bool diag = j0 + kSsTile > t.q0 + 1;   // some key of the tile may be hidden
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RW; ++i) {
+            const int row = t.q0 + ty * RW + i;
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[i][j] *= p.scale_log2;
                 // hidden keys; a row past the sequence's end sees the keys that there are
-                if (diag && (j0 + tx * 4 + j > t.q0 + ty * 4 + i || j0 + tx * 4 + j >= t.end)) s[i][j] = -INFINITY;
+                if (diag && (j0 + tx * 4 + j > row || j0 + tx * 4 + j >= t.end)) s[i][j] = -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll
@@ -133,7 +158,7 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = exp2f(s[i][j] - mn);
                 sum += s[i][j];
-                ps[(tx * 4 + j) * kSsPad + ty * 4 + i] = s[i][j];
+                ps[(tx * 4 + j) * QP + ty * RW + i] = s[i][j];
             }
             l[i] = l[i] * f + sum;   // this thread's four key columns; joined at the end
 #pragma unroll
@@ -144,38 +169,39 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
         if (!diag) {
 #pragma unroll 4
             for (int j = 0; j < kSsTile; ++j) {
-                const float4 a4 = *reinterpret_cast<const float4 *>(ps + j * kSsPad + ty * 4);
-                const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+                float a[RW];
+                lds_rows(ps + j * QP + ty * RW, a);
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     const float b = vs[j * D + tx + c * 16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i][c] = fmaf(a[i], b, o[i][c]);
+                    for (int i = 0; i < RW; ++i) o[i][c] = fmaf(a[i], b, o[i][c]);
                 }
             }
         } else {
             // a hidden key's value is left out, not multiplied by 0: it may be NaN or infinite
+#pragma unroll 4
             for (int j = 0; j < n; ++j) {
-                const float4 a4 = *reinterpret_cast<const float4 *>(ps + j * kSsPad + ty * 4);
-                const float a[4] = {a4.x, a4.y, a4.z, a4.w};
-                const int row = j0 + j - t.q0 - ty * 4;   // first row of this thread's that sees key j
+                float a[RW];
+                lds_rows(ps + j * QP + ty * RW, a);
+                const int row = j0 + j - t.q0 - ty * RW;   // first row of this thread's that sees key j
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     const float b = vs[j * D + tx + c * 16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < RW; ++i)
                         if (i >= row) o[i][c] = fmaf(a[i], b, o[i][c]);
                 }
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RW; ++i)
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = t.q0 + ty * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+        const int r = t.q0 + ty * RW + i;
         if (r < t.end) {
             OutT *dst = (OutT *)p.out + h * p.o_hs + (long)r * p.o_ts + tx;
             const float inv = 1.f / l[i];

@@ -132,7 +132,7 @@ def test_evict_refusals(L):
     assert ev(keep=0) == ev(recent=-1) == ev(recent=11) == ev(keep=13) == INVALID
     assert ev(o=cache(20, B=2)) == ev(o=cache(20, H_kv=1)) == ev(o=cache(20, d=32)) == INVALID
     assert ev(o=cache(10)) == ev(o=cache(20, v_codes=P(10))) == ev(o=cache(20, k_par=P(13))) == INVALID
-    assert ev(ws=None) == ev(nws=need - 1) == ev(ws=P(3, 32)) == INVALID
+    assert ev(kept=None, ws=None) == ev(kept=None, nws=need - 1) == ev(kept=None, ws=P(3, 32)) == INVALID
 
 
 def test_python_checks():
