@@ -411,7 +411,7 @@ class KV4Cache(typing.NamedTuple):
         return cls(*half(), *half())
 
 
-_DIMS = (32, 64, 128)
+_HALVES = (16, 32, 64)   # bytes of a row's codes
 
 
 def _need(ok, what):
@@ -422,16 +422,19 @@ def _need(ok, what):
 def _cache_c(cache, what="cache"):
     """The C view of a cache and its device index."""
     kc, kp, vc, vp = cache
-    shape = kc.shape
     dev = kc.get_device()
-    if (len(shape) != 4 or dev < 0 or kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 or vc.shape != shape
-            or shape[3] * 2 not in _DIMS or kp.dtype is not torch.int32 or vp.dtype is not torch.int32
-            or kp.shape != vp.shape or kp.dim() != 4 or kp.shape[:3] != shape[:3] or kp.shape[3] * 16 != shape[3]
+    try:
+        B, Hk, cap, half = shape = kc.shape
+    except ValueError:
+        B, Hk, cap, half = shape = (0, 0, 0, 0)
+    par = (B, Hk, cap, half >> 4)
+    if (half not in _HALVES or dev < 0 or vc.shape != shape or kp.shape != par or vp.shape != par
+            or kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8
+            or kp.dtype is not torch.int32 or vp.dtype is not torch.int32
             or kp.get_device() != dev or vc.get_device() != dev or vp.get_device() != dev
             or not (kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and vp.is_contiguous())):
         raise ValueError(f"{what}: k_codes, v_codes [B, H_kv, cap, d / 2] uint8 and k_par, v_par [B, H_kv, cap, d / 32] "
                          "int32, contiguous, on one CUDA device, d 32, 64 or 128")
-    B, Hk, cap, half = shape
     return _Kv4CacheC(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), B, Hk, cap, half * 2), dev
 
 
@@ -523,6 +526,11 @@ def _ws(workspace, need, device, dev):
         return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace: contiguous, on the tensors' device")
     return workspace
+
+
+def _out_like(x, dtype):
+    # (x is contiguous)
+    return torch.empty_like(x) if dtype is None else torch.empty_like(x, dtype=dtype)
 
 
 def _addr(x):
@@ -633,7 +641,7 @@ def la_kv4_decode(q, cache, lens, scale=None, weights_in=None, weights_out=None,
     with _On(dev, stream) as on:
         on.uses(q, lens, weights_in, weights_out, out, workspace, *cache)
         if out is None:
-            out = torch.empty(shape, dtype=dt if out_dtype is None else out_dtype, device=q.device)
+            out = _out_like(q, out_dtype)
             on.hands(out)
         ws = _ws(workspace, _decode_ws(B, H, Hk, cap, d, 0 if weights_out is None else 1), q.device, dev)
         st = lib().la_kv4_decode(

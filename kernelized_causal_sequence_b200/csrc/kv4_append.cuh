@@ -28,6 +28,7 @@ struct Kv4AppendParams {
     Kv4CacheDev c;
     int N;
     void *k_out, *v_out;    // kv4_read
+    int per;                // kv4_read: tokens of a warp
 };
 
 constexpr int kAppendThreads = 256;
@@ -62,54 +63,54 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendPar
     const long ts = keys ? p.k_ts : p.v_ts;
     uint8_t *codes = keys ? p.c.k_codes : p.c.v_codes;
     uint32_t *par = keys ? p.c.k_par : p.c.v_par;
-    const int step = gridDim.x * (kAppendThreads / 8);
-    // a warp's four rows go round together, so that its shuffles are whole
-    for (int t0 = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 5) * 4; t0 < p.N; t0 += step) {
-        const int t = t0 + ((threadIdx.x & 31) >> 3);
-        const long row = t < p.N ? kv4_row(p, t, head) : -1;
-        float v[G][4], lo[G], hi[G];
+    const int t = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 3);
+    // the values are on their way while the token's row is found
+    float v[G][4], lo[G], hi[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row >= 0) f = load4<InT>(x + (long)t * ts + g * kKv4Group + r * 4);
-            v[g][0] = f.x; v[g][1] = f.y; v[g][2] = f.z; v[g][3] = f.w;
-            lo[g] = min_nan(min_nan(f.x, f.y), min_nan(f.z, f.w));
-            hi[g] = max_nan(max_nan(f.x, f.y), max_nan(f.z, f.w));
-        }
-        // over the eight threads; with several groups each step also halves
-        // the groups that a thread goes on with (4: 8 shuffles instead of 24):
-        // thread r ends with group (r / 4) G / 2 + (r / 2) % 2 (G / 4) ...
+    for (int g = 0; g < G; ++g) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < p.N) f = load4<InT>(x + (long)t * ts + g * kKv4Group + r * 4);
+        v[g][0] = f.x; v[g][1] = f.y; v[g][2] = f.z; v[g][3] = f.w;
+    }
+    const long row = t < p.N ? kv4_row(p, t, head) : -1;
 #pragma unroll
-        for (int off = 4, n = G; off > 0; off >>= 1) {
-            if (n > 1) {
-                const bool up = r & off;
-                n >>= 1;
+    for (int g = 0; g < G; ++g) {
+        lo[g] = min_nan(min_nan(v[g][0], v[g][1]), min_nan(v[g][2], v[g][3]));
+        hi[g] = max_nan(max_nan(v[g][0], v[g][1]), max_nan(v[g][2], v[g][3]));
+    }
+    // over the eight threads; with several groups each step also halves the
+    // groups that a thread goes on with (4 groups: 12 shuffles instead of 24),
+    // so that thread r ends with group r G / 8
 #pragma unroll
-                for (int g = 0; g < n; ++g) {
-                    const float l = __shfl_xor_sync(0xffffffffu, up ? lo[g] : lo[g + n], off);
-                    const float h = __shfl_xor_sync(0xffffffffu, up ? hi[g] : hi[g + n], off);
-                    lo[g] = min_nan(up ? lo[g + n] : lo[g], l);
-                    hi[g] = max_nan(up ? hi[g + n] : hi[g], h);
-                }
-            } else {
-                lo[0] = min_nan(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], off));
-                hi[0] = max_nan(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], off));
+    for (int off = 4, n = G; off > 0; off >>= 1) {
+        if (n > 1) {
+            const bool up = r & off;
+            n >>= 1;
+#pragma unroll
+            for (int g = 0; g < n; ++g) {
+                const float l = __shfl_xor_sync(0xffffffffu, up ? lo[g] : lo[g + n], off);
+                const float h = __shfl_xor_sync(0xffffffffu, up ? hi[g] : hi[g + n], off);
+                lo[g] = min_nan(up ? lo[g + n] : lo[g], l);
+                hi[g] = max_nan(up ? hi[g + n] : hi[g], h);
             }
+        } else {
+            lo[0] = min_nan(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], off));
+            hi[0] = max_nan(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], off));
         }
-        // the word of that group (NaN in lo and hi if any value was)
-        const uint32_t own = kv4_word(lo[0], hi[0], __float_as_uint(max_nan(fabsf(lo[0]), fabsf(hi[0]))) & 0x7fffffffu);
-        uint32_t word = 0u;   // group r's, for the store
-        Chunk chunk = 0;
+    }
+    // the word of that group (NaN in lo and hi if any value was)
+    const uint32_t own = kv4_word(lo[0], hi[0], __float_as_uint(max_nan(fabsf(lo[0]), fabsf(hi[0]))) & 0x7fffffffu);
+    uint32_t word = 0u;   // group r's, for the store
+    Chunk chunk = 0;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const uint32_t w = __shfl_sync(0xffffffffu, own, g * (8 / G), 8);
-            if (r == g) word = w;
-            chunk |= (Chunk)((Chunk)kv4_codes(v[g], w) << (16 * g));
-        }
-        if (row >= 0) {
-            reinterpret_cast<Chunk *>(codes)[row * 8 + r] = chunk;
-            if (r < G) par[row * G + r] = word;
-        }
+    for (int g = 0; g < G; ++g) {
+        const uint32_t w = __shfl_sync(0xffffffffu, own, g * (8 / G), 8);
+        if (r == g) word = w;
+        chunk |= (Chunk)((Chunk)kv4_codes(v[g], w) << (16 * g));
+    }
+    if (row >= 0) {
+        reinterpret_cast<Chunk *>(codes)[row * 8 + r] = chunk;
+        if (r < G) par[row * G + r] = word;
     }
 }
 
@@ -123,9 +124,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(Kv4AppendParam
     const uint8_t *codes = keys ? p.c.k_codes : p.c.v_codes;
     const uint32_t *par = keys ? p.c.k_par : p.c.v_par;
     OutT *out = keys ? (OutT *)p.k_out : (OutT *)p.v_out;
-    const int step = gridDim.x * (kAppendThreads / 8);
-    for (int t = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 3); t < p.N; t += step) {
-        const long row = kv4_row(p, t, head);
+    // a warp takes p.per (4 to 32) tokens: its lanes find a row each, then four tokens at a time
+    const int lane = threadIdx.x & 31, w0 = (blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5)) * p.per;
+    const long rows = lane < p.per && w0 + lane < p.N ? kv4_row(p, w0 + lane, head) : -1;
+#pragma unroll 2
+    for (int i = 0; i < p.per; i += 4) {
+        const int t = w0 + i + (lane >> 3);
+        const long row = __shfl_sync(0xffffffffu, rows, i + (lane >> 3));
+        if (t >= p.N) continue;
         Chunk chunk = 0;
         if (row >= 0) chunk = reinterpret_cast<const Chunk *>(codes)[row * 8 + r];
         OutT *dst = out + ((long)head * p.N + t) * D + r * 4;

@@ -20,13 +20,13 @@
 // s and o enter in fp32, on the scores and on p.  Queries are scaled by a power
 // of two per head that brings the largest to [2^10, 2^11): 16-bit ones are then
 // one fp16 term (bf16: exact down to 2^-35 of the largest), fp32 ones two
-// (2^-23 of the largest).  p s is scaled by a power of two per tile and group,
-// so that fp16 holds it whatever the values' magnitude (at most 2^15, and to
-// 2^-32 of the tile's largest scale), and rounded once (16-bit queries; 2^-11
-// of itself) or carried as two terms (fp32); the second sum uses the same
-// rounded number.  Tensor-core sums run over one tile of 32 positions only and
-// are joined in fp32: the tensor core cuts its sums off instead of rounding,
-// which over a long cache would add up.
+// (2^-23 of the largest).  p s is scaled by a power of two, so that fp16 holds
+// it whatever the values' magnitude (at most 2^15, and to 2^-32 of the largest
+// scale), and rounded once (16-bit queries; 2^-11 of itself) or carried as two
+// terms (fp32); the second sum uses the same rounded number.  With fp32 queries
+// tensor-core sums run over one tile of 32 positions only and are joined in
+// fp32: the tensor core cuts its sums off instead of rounding, 2^-24 of them
+// each time, which over a long cache would be seen at fp32's precision.
 //
 // A warp takes tiles of 32 positions through a ring of its own in shared
 // memory, filled by cp.async.  Each lane first turns one position's parameter
@@ -44,8 +44,8 @@
 // line that is cut into equal pieces, one per resident CTA (DecLine).  A CTA
 // walks its piece row by row, its warps take turns at the tiles and join at
 // the row's end; a row cut between CTAs is joined by kv4_finish_kernel.
-// Caches of at most kDecWhole positions are dealt out by whole rows instead and
-// need no second kernel.
+// Short caches are dealt out by whole rows instead and need no second kernel
+// (16 x 16 rows, lengths to 2048 at d 64: 18.0 / 16.5 us).
 #pragma once
 #include <type_traits>
 
@@ -74,8 +74,11 @@ struct Kv4DecodeParams {
 constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2;
 constexpr float kDecLazy = 8.f;
 constexpr int kDecCtas = 3;         // CTAs per SM with up to 8 query heads (more: 2)
-constexpr int kDecMinTiles = 16;    // tiles of a CTA at least: four per warp, to hide its start
-constexpr int kDecWhole = 512;      // positions up to which a row is not cut
+constexpr int kDecMinTiles = 16;    // places of a CTA at least: three or four tiles a warp, to hide its start
+constexpr int kDecRowCost = 8;      // tiles' worth of time (of four warps) that a row's start and join take
+                                    // (64 rows x 4, lengths to 8192: 0 66.9 us, 4 64.5, 8 63.9, 12 64.0)
+constexpr int kDecWhole = 512, kDecWholeFull = 2048;   // positions up to which a row is not cut: always, and
+                                                       // where there is a row for every SM
 
 // Row i of a 16-row tile holds this position of it: odd pairs are swapped, so
 // that rows 0, 2, 4, 6 (one value load of a warp) alternate between even and
@@ -179,19 +182,22 @@ template <int D> constexpr size_t kv4_decode_smem(int nt) {
     return ring > join ? ring : join;
 }
 
-// The line of tiles: sequence b begins at rows_per_seq * (tiles of the sequences before it).
+// The line: a row takes as many places as it has tiles, and kDecRowCost more for
+// its start and join; sequence b begins at rows_per_seq * (places of a row of
+// each sequence before it).
 struct DecLine {
     int rows;    // rows of a sequence
-    int chunk;   // tiles of a CTA
+    int chunk;   // places of a CTA
     long total;
 };
 __device__ __forceinline__ int dec_len(const int32_t *lens, int b, int cap) { return min(max(lens[b], 0), cap); }
 __device__ __forceinline__ int dec_tiles(int n) { return (n + kDecTile - 1) / kDecTile; }
+__device__ __forceinline__ int dec_places(int n) { return n > 0 ? dec_tiles(n) + kDecRowCost : 0; }
 
-// Tiles of sequences [0, b); whole warp.
-__device__ __forceinline__ long dec_tiles_before(const Kv4DecodeParams &p, int b) {
+// Places of a row of each of the sequences [0, b); whole warp.
+__device__ __forceinline__ long dec_places_before(const Kv4DecodeParams &p, int b) {
     long sum = 0;
-    for (int i = threadIdx.x & 31; i < b; i += 32) sum += dec_tiles(dec_len(p.lens, i, p.c.cap));
+    for (int i = threadIdx.x & 31; i < b; i += 32) sum += dec_places(dec_len(p.lens, i, p.c.cap));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     return sum;
@@ -199,17 +205,17 @@ __device__ __forceinline__ long dec_tiles_before(const Kv4DecodeParams &p, int b
 __device__ __forceinline__ DecLine dec_line(const Kv4DecodeParams &p) {
     DecLine d;
     d.rows = p.c.Hkv * p.head_blocks;
-    d.total = dec_tiles_before(p, p.c.B) * d.rows;
+    d.total = dec_places_before(p, p.c.B) * d.rows;
     const long c = (d.total + p.n_cta - 1) / p.n_cta;
     d.chunk = (int)max(c, (long)kDecMinTiles);
     return d;
 }
-// The sequence that holds place `at` < total of the line, and the tiles before it; whole warp.
+// The sequence that holds place `at` < total of the line, and the places of a row of those before it; whole warp.
 __device__ __forceinline__ int dec_find(const Kv4DecodeParams &p, const DecLine &d, long at, long *before) {
     const int lane = threadIdx.x & 31;
     long sum = 0;
     for (int b0 = 0;; b0 += 32) {
-        const int nt = b0 + lane < p.c.B ? dec_tiles(dec_len(p.lens, b0 + lane, p.c.cap)) : 0;
+        const int nt = b0 + lane < p.c.B ? dec_places(dec_len(p.lens, b0 + lane, p.c.cap)) : 0;
         long x = nt;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -234,6 +240,7 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
     constexpr int G = C::G, HB = 8 * NT;
     constexpr int QT = std::is_same<InT, float>::value ? 2 : 1;   // terms of a query
     constexpr int PT = QT;                                        // terms of p s
+    constexpr bool TILE_SUMS = PT > 1;                            // tensor-core sums over one tile only
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, cq = lane & 3;
     const int hk = row / p.head_blocks, hb = row % p.head_blocks;
@@ -346,6 +353,9 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
 #pragma unroll
         for (int g = 0; g < G; ++g) ob[nt][g] = 0.f;
     }
+    // warp-wide: the power of two in which p s is held, and the scale's bits from which it is too small
+    float unit = 0.f, per_unit = 0.f;
+    uint32_t unit_end = 0u;
     int stage = 0;
 #pragma unroll 1
     for (int tile = warp; tile < n_tiles; tile += kDecWarps) {
@@ -358,7 +368,6 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
         stage = stage == kDecStages - 1 ? 0 : stage + 1;
         const int t0 = t_begin + tile * kDecTile;
         // ---- parameters: this lane's position
-        float unit;   // warp-wide: the power of two in which the tile's p s are held
         {
             uint32_t kw[G], vw[G];
             lds_words(st + C::OFF_KP + lane * 4 * G, kw);
@@ -366,10 +375,24 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
             uint32_t big = 0u;
 #pragma unroll
             for (int g = 0; g < G; ++g) big = max(big, vw[g] << 16);
-            // the largest scale is in [2^e, 2^(e + 1)): p s < 2^8 2^(e + 1) = 2^15 unit
-            const uint32_t e = max(__reduce_max_sync(0xffffffffu, big) >> 23, 7u);
-            unit = __uint_as_float((e - 6u) << 23);
-            const float per_unit = __uint_as_float((260u - e) << 23);
+            // The unit grows with the largest scale met (in [2^e, 2^(e + 1)): p s < 2^8 2^(e + 1) = 2^15 unit);
+            // one-term queries sum their products in it from tile to tile.
+            if (TILE_SUMS || __any_sync(0xffffffffu, big >= unit_end)) {
+                const uint32_t e = max(__reduce_max_sync(0xffffffffu, big) >> 23, 7u);
+                const float old = unit;
+                unit = __uint_as_float((e - 6u) << 23);
+                per_unit = __uint_as_float((260u - e) << 23);
+                unit_end = (e + 1u) << 23;
+                if (!TILE_SUMS && old > 0.f) {
+                    const float f = old / unit;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2 * G; ++k)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[nt][k][i] *= f;
+                }
+            }
             float x[4][G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -530,7 +553,11 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
                 }
             }
         }
-        float ot[NT][2 * G][4];   // this tile's outputs, in units
+        float tile_sums[TILE_SUMS ? NT : 1][TILE_SUMS ? 2 * G : 1][4];
+        auto &ot = [&]() -> auto & {
+            if constexpr (TILE_SUMS) return tile_sums;
+            else return o;
+        }();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float vs[4][G], vo[4][G];   // scale / unit, (offset + 8) unit of rows 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9
@@ -556,7 +583,7 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
                         const float2 u = unpack_h2(b0), w = unpack_h2(b1);
                         ob[nt][g] = fmaf(u.x, vo[0][g], fmaf(u.y, vo[1][g], fmaf(w.x, vo[2][g], fmaf(w.y, vo[3][g], ob[nt][g]))));
                         if (t + 1 < PT) { x[0] -= u.x; x[1] -= u.y; x[2] -= w.x; x[3] -= w.y; }
-                        if (half == 0 && t == 0) {
+                        if (TILE_SUMS && half == 0 && t == 0) {
                             mma_f16_first(ot[nt][2 * g], nl[0], nl[1], nh[0], nh[1], b0, b1);
                             mma_f16_first(ot[nt][2 * g + 1], nl[2], nl[3], nh[2], nh[3], b0, b1);
                         } else {
@@ -567,17 +594,27 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
                 }
             }
         }
+        if constexpr (TILE_SUMS) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 2 * G; ++k)
+                for (int k = 0; k < 2 * G; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[nt][k][i] = fmaf(ot[nt][k][i], unit, o[nt][k][i]);
+                    for (int i = 0; i < 4; ++i) o[nt][k][i] = fmaf(ot[nt][k][i], unit, o[nt][k][i]);
+        }
         __syncwarp();   // the tile has been read: the next turn's loads and parameters overwrite it
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();    // the rings are done: their memory joins the warps
 
+    if constexpr (!TILE_SUMS) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2 * G; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][k][i] *= unit;
+    }
     // ---- join the warps: [warp][head][D], then [warp][head] (m, l)
     float *jo = reinterpret_cast<float *>(dec_smem);
     float2 *jml = reinterpret_cast<float2 *>(jo + kDecWarps * HB * D);
@@ -666,10 +703,12 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
     long before;
     int b = dec_find(p, d, at, &before);
     int n = dec_len(p.lens, b, p.c.cap), nt = dec_tiles(n);
-    long off = at - before * rows;
-    int row = (int)(off / nt), tile = (int)(off % nt);
-    while (at < end) {
-        if (tile == nt) {
+    const long off = at - before * rows;
+    int row = (int)(off / dec_places(n)), tile = (int)(off % dec_places(n));
+    while (true) {
+        if (tile >= nt) {   // the next row
+            at += nt + kDecRowCost - tile;
+            if (at >= end) return;
             tile = 0;
             if (++row == rows) {
                 row = 0;
@@ -683,6 +722,7 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
         decode_row<InT, OutT, D, NT>(p, dec_smem, b, row, n, tile, count, slot);
         at += count;
         tile += count;
+        if (at >= end) return;
     }
 }
 
@@ -690,8 +730,8 @@ kv4_decode_kernel(const Kv4DecodeParams p) {
 // x < out_blocks of a (key/value head, sequence): outputs; the others: weights.
 constexpr int kFinThreads = 256;
 
-// The pieces of a row of the line that begins at place `start` with nt tiles:
-// the CTAs first .. last; slot of a CTA's piece.
+// The pieces of a row that begins at place `start` of the line: the CTAs first
+// .. last that have tiles of it; slot of a CTA's piece.
 struct DecPieces {
     int first, last;
     long start;
@@ -704,19 +744,19 @@ __global__ void __launch_bounds__(kFinThreads) kv4_finish_kernel(const Kv4Decode
     pdl_wait();
     const int hk = blockIdx.y, b = blockIdx.z;
     const int n = dec_len(p.lens, b, p.c.cap), nt = dec_tiles(n);
-    if (n == 0) return;
     const int HB = p.head_block;
     const long h0 = (long)b * p.H + (long)hk * p.group;
     DecLine d{0, 1, 0};
     long before = 0;
     if (!p.whole) {
         d = dec_line(p);
-        before = dec_tiles_before(p, b);
+        before = dec_places_before(p, b);
     }
+    if (n == 0) return;
     auto pieces = [&](int head) {   // of the row that holds the query head
         DecPieces x{0, 0, 0, d.chunk};
         if (!p.whole) {
-            x.start = before * d.rows + (long)(hk * p.head_blocks + head / HB) * nt;
+            x.start = before * d.rows + (long)(hk * p.head_blocks + head / HB) * (nt + kDecRowCost);
             x.first = (int)(x.start / d.chunk);
             x.last = (int)((x.start + nt - 1) / d.chunk);
         }

@@ -122,12 +122,16 @@ la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
     return run_softmax_simt_bm<InT, OutT, 16>(p, d, st);
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
-    const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
+    const dim3 grid((unsigned)((p.N + kAppendThreads / 8 - 1) / (kAppendThreads / 8)), (unsigned)p.c.Hkv, 2);
     LA_BY_D(d, return launch_kernel(kv4_append_kernel<InT, D>, grid, dim3(kAppendThreads), 0, st, true,
                                     "kv4 append launch", p))
 }
-template <typename OutT> la_status run_read(const Kv4AppendParams &p, int d, cudaStream_t st) {
-    const dim3 grid(stride_grid(p.N, kAppendThreads / 8, 2L * p.c.Hkv), (unsigned)p.c.Hkv, 2);
+template <typename OutT> la_status run_read(Kv4AppendParams p, int d, cudaStream_t st) {
+    // as many tokens a warp as leave 40 warps for every SM
+    p.per = 4;
+    while (p.per < 32 && (long)p.N * p.c.Hkv * 2 / (2 * p.per) >= 40L * kNumSMs) p.per *= 2;
+    const int block = kAppendThreads / 32 * p.per;
+    const dim3 grid((unsigned)((p.N + block - 1) / block), (unsigned)p.c.Hkv, 2);
     LA_BY_D(d, return launch_kernel(kv4_read_kernel<OutT, D>, grid, dim3(kAppendThreads), 0, st, true,
                                     "kv4 read launch", p))
 }
@@ -142,8 +146,8 @@ DecodePlan decode_plan(int B, int H, int H_kv, int cap, int d, int with_weights)
     const int group = H / H_kv;
     w.nt = group > 8 ? 2 : 1;
     w.head_blocks = (group + 8 * w.nt - 1) / (8 * w.nt);
-    w.whole = cap <= kDecWhole;
     const long rows = (long)B * H_kv * w.head_blocks;
+    w.whole = cap <= (rows >= kNumSMs ? kDecWholeFull : kDecWhole);
     w.n_cta = w.whole ? (int)rows : kNumSMs * (w.nt == 1 ? kDecCtas : 2);
     size_t at = 0;
     w.ml_off = at;
