@@ -224,7 +224,8 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
     p.scale_log2 = scale * kLog2e;
     p.status = (int *)workspace;
     if (softmax_tc_supported(in_dtype, d)) {
-        if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 2 * sizeof(int), st))) != LA_OK) return s;
+        // the status word and the tile counter behind it
+        if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 4 * sizeof(int), st))) != LA_OK) return s;
         return softmax_tc(p, in_dtype, out_dtype, d, (int *)workspace, wait_limit_ns(), st);
     }
     LA_BY_TYPES(in_dtype, out_dtype, return (run_softmax_simt<InT, OutT>(p, d, st)))

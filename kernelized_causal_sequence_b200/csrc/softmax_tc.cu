@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "launch.h"
+#include "plan.h"
 #include "softmax_tc.cuh"
 #include "softmax_tc.h"
 
@@ -51,9 +52,11 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long l
     p.H = sp.H; p.group = sp.group; p.N = sp.N; p.n_seq = sp.n_seq;
     p.tiles = seq_tiles(sp.N, sp.n_seq, MODE == stc::kTwoTiles ? 256 : 128);
     p.scale_log2 = sp.scale_log2; p.status = status; p.wait_ns = wait_ns;
-    const long grid = (long)p.tiles * (MODE == stc::kTwoHeads ? sp.H / 2 : sp.H);
-    if (grid > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
+    const long tiles = (long)p.tiles * (MODE == stc::kTwoHeads ? sp.H / 2 : sp.H);
+    if (tiles > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
     using G = stc::Cfg<D, MODE>;
+    const long resident = kNumSMs * (G::SLOTS == 1 ? 2 : 1);
+    const long grid = tiles < resident ? tiles : resident;
     return launch_kernel(stc::softmax_tc_kernel<InT, OutT, D, MODE>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st,
                          false, "softmax tensor-core launch", mq, mk, mv, (const InT *)sp.v, sp.v_hs, sp.v_ts, p);
 }

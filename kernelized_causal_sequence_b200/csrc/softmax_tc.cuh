@@ -1,11 +1,10 @@
 // softmax_tc.cuh — causal softmax attention over packed sequences on the
 // tensor cores (bf16/fp16 inputs, head dim 64 or 128, fp32 sums).
 //
-// A CTA holds two tiles ("slots") of 128 queries that read the same keys and
-// values: the same rows of two query heads that share a key/value head where
-// heads are shared evenly (PAIR), else 256 consecutive rows of one head.  It
-// walks the keys in blocks of 128 from the sequence's begin to the tile's
-// diagonal.  Per slot and block j, with c = scale log2(e):
+// A CTA holds one or two tiles ("slots") of 128 queries that read the same keys
+// and values (enum Slots), and walks the keys in blocks of 128 from the
+// sequence's begin to the tile's diagonal.  Per slot and block j, with
+// c = scale log2(e):
 //
 //   S = Q K_j^T                     tcgen05, fp32 in TMEM
 //   m' = max(m, rowmax S)           the reference of the exponents moves only
@@ -20,17 +19,25 @@
 // rounding depends on it), so it is moved only beyond that: after the first
 // blocks almost never.
 //
-// The two slots alternate on the tensor core: while one slot's exponentials
-// run, the products of the other do.  With 128 x 128 scores per block the
-// exponentials (16 a clock and SM on the special-function unit) take as long
-// as both products at d 128 and twice as long at d 64, so part of them is
-// computed by a polynomial on the FMA units (exp2_poly).
+// The two slots (or two CTAs of one) alternate on the tensor core: while one
+// slot's exponentials run, the products of the other do.  At d 128 the products
+// are the bound (leaving all exponentials out changes a long prompt's time by
+// 1%); they run at what the tensor core gets from shared memory, whose reads
+// for Q K^T (8 KB per 128 x 128 x 16 product) and P V and whose fills together
+// take as long as the products.  At d 64 the products are half as long and the
+// softmax is the bound (226 us with, 170 us without it: 8192 tokens, 16 heads).
+// Computing part of the exponentials on the FMA units gained nothing: a warp's
+// issue, not the special-function unit, sets the softmax's pace.
 //
-// Warps (352 threads, one CTA per SM):
-//   0-3, 4-7   softmax of slot 0, 1: a thread owns one row (TMEM lane)
-//   8          TMA producer (one thread): Q, then K_0, V_0, K_1, V_1, ...
-//   9          TMEM allocation, MMA issue (one thread)
-//   10         the values of a diagonal block: rows behind the sequence are
+// CTAs stay resident and take tiles from one list (a counter in the workspace):
+// the copies and the first products of the next tile run during the softmax and
+// the output of the last.
+//
+// Warps (S = 4 per slot softmax warps, then):
+//   softmax    a thread owns one row (TMEM lane)
+//   S          the list and the TMA copies (one thread): K_0, Q, V_0, K_1, ...
+//   S + 1      TMEM allocation, MMA issue (one thread)
+//   S + 2      the values of a diagonal block: rows behind the sequence are
 //              zeroed, and NaN or infinities taken out, since P = 0 does not
 //              hide them from the product; the rows that see them get them
 //              back at the end (restore_nonfinite)
@@ -70,19 +77,29 @@ template <int D, int MODE> struct Cfg {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = SLOTS * TILE;
     static constexpr int OFF_BAR = OFF_KV + NST * TILE;
-    static constexpr int B_Q = 0, B_KV_FULL = 2, B_KV_EMPTY = B_KV_FULL + NST, B_S = B_KV_EMPTY + NST;
-    static constexpr int B_P = B_S + 2, B_O = B_P + 2, B_CLEAN = B_O + 2;
-    // a diagonal block's values have a full barrier of their own: the scrub warp
-    // does not follow the ring's phases (they are the last use of their stages)
-    static constexpr int B_VD = B_CLEAN + 2, B_DRAIN = B_VD + 2;
+    // barriers: Q of a slot full / empty, ring stages full / empty, S, P, O of a slot full, O of a slot empty
+    static constexpr int B_Q = 0, B_Q_EMPTY = 2, B_KV_FULL = 4, B_KV_EMPTY = B_KV_FULL + NST, B_S = B_KV_EMPTY + NST;
+    static constexpr int B_P = B_S + 2, B_O = B_P + 2, B_O_EMPTY = B_O + 2;
+    // A diagonal block's values have full barriers of their own (by turns; more
+    // than can be in the ring at once), as the scrub warp does not follow the
+    // ring's phases; and one each for "scrubbed".
+    static constexpr int B_VD = B_O_EMPTY + 2, B_CLEAN = B_VD + 4;
+    static constexpr int B_WORK = B_CLEAN + 4, B_WORK_EMPTY = B_WORK + 4;   // the list of tiles
+    static constexpr int B_DRAIN = B_WORK_EMPTY + 4;
     static constexpr int NBAR = B_DRAIN + 1;
     static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 4;
-    static constexpr int OFF_FLAG = OFF_ABORT + 4;     // two ints: a diagonal block held NaN or infinities
-    static constexpr int SMEM = OFF_FLAG + 8 + 1024;   // + alignment
+    static constexpr int OFF_WORK = (OFF_ABORT + 4 + 15) / 16 * 16;   // [4] Work
+    static constexpr int OFF_FLAG = OFF_WORK + 4 * 16;                // [4][2] ints: a diagonal block held NaN or infinities
+    static constexpr int SMEM = OFF_FLAG + 4 * 8 + 1024;              // + alignment
     // TMEM: S / P of slot s at 128 s, O behind them (two CTAs of one slot each share the 512 columns)
     static constexpr int T_S = 0, T_O = 128 * SLOTS, TMEM_COLS = 256 * SLOTS;
     static_assert(SMEM <= (SLOTS == 1 ? 115712 : 232448), "shared memory");
+};
+
+// One tile of the list: a sequence's tokens, the tile's first, its (first) head; head < 0 ends the list.
+struct Work {
+    int begin, end, q0, head;
 };
 
 struct Params {
@@ -91,7 +108,7 @@ struct Params {
     long o_hs, o_ts;
     int H, group, N, n_seq, tiles;
     float scale_log2;
-    int *status;
+    int *status;   // [0], [1] the status word, [2] the next tile
     unsigned long long wait_ns;
 };
 
@@ -185,6 +202,13 @@ __device__ __forceinline__ void restore_nonfinite(uint32_t t_o, const InT *v, lo
     tmem_st_wait();
 }
 
+// The one thread of a warp that issues for it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // mbar_wait without a call: a kernel that redistributes its registers may not
 // call functions.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const AbortCtx &ab, int code) {
@@ -207,7 +231,6 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const __grid_constant__ CUtensorMap tm_v, const InT *__restrict__ v_gmem, long v_hs, long v_ts,
                   const Params p) {
     using G = Cfg<D, MODE>;
-    constexpr bool PAIR = MODE == kTwoHeads;
     extern __shared__ uint8_t stc_smem_raw[];
     uint8_t *smem = stc_smem_raw + ((1024u - (smem_u32(stc_smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + G::OFF_BAR);
@@ -216,24 +239,15 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     volatile int *flag = reinterpret_cast<volatile int *>(smem + G::OFF_FLAG);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the work: heads fastest (CTAs that run together share keys), late tiles,
-    // which have the most keys, first
-    const int nhp = PAIR ? p.H / 2 : p.H;
-    const int hp = blockIdx.x % nhp, tile = p.tiles - 1 - blockIdx.x / nhp;
-    const SeqTile t = seq_tile<MODE == kTwoTiles ? 256 : 128>(p.cu, p.n_seq, p.N, tile);
-    if (t.q0 >= t.end) return;
-    const int h0 = PAIR ? 2 * hp : hp, hk = h0 / p.group;
-    // blocks of each slot; the last is the diagonal one
-    const int n0 = (t.q0 - t.begin) / kBlock + 1;
-    const int n1 = PAIR ? n0 : MODE == kTwoTiles && t.q0 + kBlock < t.end ? n0 + 1 : 0;
-    const int nb = max(n0, n1);
-    const int n_diag = n1 > n0 ? 2 : 1;   // diagonal blocks: n0 - 1 and, with two row tiles, n0
-
     AbortCtx ab{abort_flag, p.status, p.wait_ns};
+    volatile Work *work = reinterpret_cast<volatile Work *>(smem + G::OFF_WORK);
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        flag[0] = flag[1] = 0;
-        for (int i = 0; i < G::NBAR; ++i) mbar_init(&bar[i], (i == G::B_P || i == G::B_P + 1) ? 4 : 1);
+        for (int i = 0; i < G::NBAR; ++i) {
+            const bool soft = (i >= G::B_P && i < G::B_P + 2) || (i >= G::B_O_EMPTY && i < G::B_O_EMPTY + 2);
+            const bool list = i >= G::B_WORK_EMPTY && i < G::B_WORK_EMPTY + 4;
+            mbar_init(&bar[i], soft ? 4 : list ? 4 * G::SLOTS + 2 : 1);
+        }
         fence_mbar_init();
     }
     if (warp == G::MMA_WARP) tmem_alloc(tmem_addr, G::TMEM_COLS);
@@ -246,251 +260,351 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_addr;
+
+    // blocks of the slots in a tile; the last of each is the diagonal one
+    auto blocks0 = [](const Work &w) { return (w.q0 - w.begin) / kBlock + 1; };
+    auto blocks1 = [&](const Work &w, int n0) {
+        return MODE == kTwoHeads ? n0 : MODE == kTwoTiles && w.q0 + kBlock < w.end ? n0 + 1 : 0;
+    };
+    // Entry k of the list, or head < 0 (the end, or giving up).
+    auto next_work = [&](int k) {
+        Work w{0, 0, 0, -1};
+        if (wait_bar(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10)) {
+            w.begin = work[k & 3].begin;
+            w.end = work[k & 3].end;
+            w.q0 = work[k & 3].q0;
+            w.head = work[k & 3].head;
+        }
+        return w;
+    };
+
     // One slot: the softmax warps need more registers than the 128 that two
     // CTAs of 256 threads leave each; 128 x 200 + 128 x 56 is what there is.
     // (Two slots: 352 threads have 168, which is enough.)
     if (warp >= G::TMA_WARP) {
     if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == G::TMA_WARP) {
+        // ================= the list of tiles, and the copies
         if (lane == 0) {
-            int issued = 0;
-            for (int s = 0; s < 2; ++s) {
-                if (s == 1 && n1 == 0) continue;
-                mbar_expect_tx(&bar[G::B_Q + s], G::TILE);
-                for (int b = 0; b < G::KB; ++b)
-                    tma_load_3d(smem + G::OFF_Q + s * G::TILE + b * G::BOXB, &tm_q, &bar[G::B_Q + s], 64 * b,
-                                PAIR ? t.q0 : t.q0 + s * kBlock, PAIR ? h0 + s : h0);
-                // K_0 between the two: the first product needs Q of slot 0 and K_0
-                if (s == 0) {
-                    mbar_expect_tx(&bar[G::B_KV_FULL], G::TILE);
-                    for (int b = 0; b < G::KB; ++b)
-                        tma_load_3d(smem + G::OFF_KV + b * G::BOXB, &tm_k, &bar[G::B_KV_FULL], 64 * b, t.begin, hk);
-                    issued = 1;
+            int it = 0, diag = 0, nq[2] = {0, 0};   // ring items, diagonal blocks, query tiles of a slot so far
+            uint32_t kv_phase = 0u, last_vd = 0u;   // per stage: parity of its last ring copy; stages whose last copy was diagonal
+            const int nhp = MODE == kTwoHeads ? p.H / 2 : p.H;
+            const unsigned total = (unsigned)p.tiles * nhp;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                // heads fastest (CTAs that run together share keys), late tiles,
+                // which have the most keys, first
+                Work w{0, 0, 0, -1};
+                while (true) {
+                    const unsigned x = atomicAdd(reinterpret_cast<unsigned *>(p.status) + 2, 1u);
+                    if (x >= total) break;
+                    const SeqTile t = seq_tile<MODE == kTwoTiles ? 256 : 128>(p.cu, p.n_seq, p.N, p.tiles - 1 - (int)(x / nhp));
+                    if (t.q0 < t.end) {
+                        w = Work{t.begin, t.end, t.q0, (int)(x % nhp) * (MODE == kTwoHeads ? 2 : 1)};
+                        break;
+                    }
                 }
-            }
-            for (int i = 1; i < 2 * nb; ++i) {
-                const int st = i % G::NST, use = i / G::NST;
-                if (use > 0 && !wait_bar(&bar[G::B_KV_EMPTY + st], (use - 1) & 1, ab, 1)) break;
-                const int dg = (i >> 1) - (n0 - 1);
-                uint64_t *full = &bar[(i & 1) && dg >= 0 ? G::B_VD + dg : G::B_KV_FULL + st];
-                mbar_expect_tx(full, G::TILE);
-                issued = i + 1;
-                for (int b = 0; b < G::KB; ++b)
-                    tma_load_3d(smem + G::OFF_KV + st * G::TILE + b * G::BOXB, (i & 1) ? &tm_v : &tm_k, full, 64 * b,
-                                t.begin + (i >> 1) * kBlock, hk);
+                if (k >= 4 && !wait_bar(&bar[G::B_WORK_EMPTY + (k & 3)], ((k >> 2) - 1) & 1, ab, 11)) break;
+                work[k & 3].begin = w.begin;
+                work[k & 3].end = w.end;
+                work[k & 3].q0 = w.q0;
+                work[k & 3].head = w.head;
+                mbar_arrive(&bar[G::B_WORK + (k & 3)]);
+                if (w.head < 0) break;
+                const int n0 = blocks0(w), n1 = blocks1(w, n0), nb = max(n0, n1), hk = w.head / p.group;
+                for (int i = 0; i < 2 * nb; ++i, ++it) {
+                    const int st = it % G::NST, use = it / G::NST;
+                    if (use > 0 && !(ok = wait_bar(&bar[G::B_KV_EMPTY + st], (use - 1) & 1, ab, 1))) break;
+                    const bool vd = (i & 1) && (i >> 1) >= n0 - 1;
+                    uint64_t *full = &bar[vd ? G::B_VD + (diag & 3) : G::B_KV_FULL + st];
+                    if (vd) {
+                        ++diag;
+                        last_vd |= 1u << st;
+                    } else {
+                        kv_phase ^= 1u << st;
+                        last_vd &= ~(1u << st);
+                    }
+                    mbar_expect_tx(full, G::TILE);
+                    for (int b = 0; b < G::KB; ++b)
+                        tma_load_3d(smem + G::OFF_KV + st * G::TILE + b * G::BOXB, (i & 1) ? &tm_v : &tm_k, full, 64 * b,
+                                    w.begin + (i >> 1) * kBlock, hk);
+                    if (i > 0) continue;
+                    // the queries behind the first keys: their places free later than the ring's
+#pragma unroll
+                    for (int s = 0; s < G::SLOTS; ++s) {
+                        if ((s == 1 && n1 == 0) || !ok) continue;
+                        if (nq[s] > 0 && !(ok = wait_bar(&bar[G::B_Q_EMPTY + s], (nq[s] - 1) & 1, ab, 12))) continue;
+                        ++nq[s];
+                        mbar_expect_tx(&bar[G::B_Q + s], G::TILE);
+                        for (int b = 0; b < G::KB; ++b)
+                            tma_load_3d(smem + G::OFF_Q + s * G::TILE + b * G::BOXB, &tm_q, &bar[G::B_Q + s], 64 * b,
+                                        MODE == kTwoTiles ? w.q0 + s * kBlock : w.q0, MODE == kTwoHeads ? w.head + s : w.head);
+                    }
+                    if (!ok) { ++it; break; }
+                }
             }
             // every copy issued has completed before the CTA exits (each is waited
             // for by its reader too, unless that gave up)
             volatile int never = 0;
             AbortCtx timed{&never, nullptr, kDrainLimitNs};
-            wait_bar(&bar[G::B_Q], 0, timed, 0);
-            if (n1 > 0) wait_bar(&bar[G::B_Q + 1], 0, timed, 0);
-            for (int i = max(0, issued - G::NST); i < issued; ++i) {
-                const int dg = (i >> 1) - (n0 - 1);
-                if ((i & 1) && dg >= 0) wait_bar(&bar[G::B_VD + dg], 0, timed, 0);
-                else wait_bar(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, timed, 0);
-            }
+            for (int s = 0; s < G::SLOTS; ++s)
+                if (nq[s] > 0) wait_bar(&bar[G::B_Q + s], (nq[s] - 1) & 1, timed, 0);
+            for (int st = 0; st < min(it, G::NST); ++st)
+                if (!((last_vd >> st) & 1)) wait_bar(&bar[G::B_KV_FULL + st], ((kv_phase >> st) & 1) ^ 1, timed, 0);
+            for (int d = max(0, diag - 4); d < diag; ++d) wait_bar(&bar[G::B_VD + (d & 3)], (d >> 2) & 1, timed, 0);
         }
     } else if (warp == G::MMA_WARP) {
-        if (lane == 0) {
-            constexpr bool BF = std::is_same<InT, bf16>::value;
-            constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
-            constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
-            const uint32_t sb = smem_u32(smem);
-            auto full = [&](int i) { return wait_bar(&bar[G::B_KV_FULL + i % G::NST], (i / G::NST) & 1, ab, 2); };
-            auto product_s = [&](int s, int j) {
-                const uint64_t a = sdesc_sw128(sb + G::OFF_Q + s * G::TILE, 16, 1024);
-                const uint64_t b = sdesc_sw128(sb + G::OFF_KV + (2 * j % G::NST) * G::TILE, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * G::BOXB + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + G::T_S + 128 * s, a + off, b + off, ID_S, kk > 0);
+        // The whole warp goes through the waits and the index arithmetic, so that
+        // the descriptors are uniform values, ready before the last wait; one
+        // thread issues the products and the commits.
+        constexpr bool BF = std::is_same<InT, bf16>::value;
+        constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
+        constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
+        const uint32_t sb = smem_u32(smem);
+        const bool leader = elect_one();
+        // bits: parity of a stage's next ring copy; of a slot's next tile and block; whether it had a tile
+        uint32_t kv_phase = 0u, tile_phase = 0u, block_phase = 0u, had = 0u;
+        int it0 = 0, diag = 0;   // ring items, diagonal blocks so far
+        bool ok = true;
+        auto ring_full = [&](int st) {
+            const bool f = wait_bar(&bar[G::B_KV_FULL + st], (kv_phase >> st) & 1, ab, 2);
+            kv_phase ^= 1u << st;
+            return f;
+        };
+        for (int k = 0; ok; ++k) {
+            const Work w = next_work(k);
+            if (w.head < 0) break;
+            __syncwarp();
+            if (leader) mbar_arrive(&bar[G::B_WORK_EMPTY + (k & 3)]);
+            const int n0 = blocks0(w), n1 = blocks1(w, n0), nb = max(n0, n1);
+            // step j: per slot P V_j, then S of block j + 1
+            int sv = (it0 + G::NST - 1) % G::NST, sk = it0 % G::NST;   // stages of V_j and K_{j+1}
+#pragma unroll 1
+            for (int j = -1; j < nb; ++j) {
+                if (j >= n0 - 1 && j >= 0) {
+                    ok = wait_bar(&bar[G::B_CLEAN + (diag & 3)], (diag >> 2) & 1, ab, 4);
+                    ++diag;
+                } else if (j >= 0) {
+                    ok = ring_full(sv);
                 }
-                mma_commit(&bar[G::B_S + s]);
-            };
-            bool ok = full(0);
-            for (int s = 0; s < 2 && ok; ++s) {
-                if (s == 1 && n1 == 0) continue;
-                ok = wait_bar(&bar[G::B_Q + s], 0, ab, 3);
-                if (!ok) break;
-                tc_fence_after();
-                product_s(s, 0);
-            }
-            if (ok) mma_commit(&bar[G::B_KV_EMPTY]);
-            for (int j = 0; j < nb && ok; ++j) {
-                const int st_v = (2 * j + 1) % G::NST, st_k = (2 * j + 2) % G::NST;
-                for (int s = 0; s < 2 && ok; ++s) {
+                if (ok && j + 1 < nb) ok = ring_full(sk);
+                const uint64_t bv = sdesc_sw128(sb + G::OFF_KV + sv * G::TILE, G::BOXB, 1024);
+                const uint64_t bk = sdesc_sw128(sb + G::OFF_KV + sk * G::TILE, 16, 1024);
+#pragma unroll
+                for (int s = 0; s < G::SLOTS; ++s) {
                     const int n = s ? n1 : n0;
-                    if (j >= n) continue;
-                    ok = (j < n0 - 1 ? full(2 * j + 1) : wait_bar(&bar[G::B_CLEAN + j - (n0 - 1)], 0, ab, 4)) &&
-                         wait_bar(&bar[G::B_P + s], j & 1, ab, 5);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t bv = sdesc_sw128(sb + G::OFF_KV + st_v * G::TILE, G::BOXB, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < kBlock / 16; ++kk) {
-                        mma_ts(tmem + G::T_O + 128 * s, tmem + G::T_S + 128 * s + kk * 8,
-                               bv + (uint64_t)((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                    if (n == 0 || j >= n || !ok) continue;
+                    const uint32_t to = tmem + G::T_O + 128 * s, ts = tmem + G::T_S + 128 * s;
+                    if (j >= 0) {
+                        // (a new tile's first product overwrites O: its last one has been read out)
+                        if (j == 0 && ((had >> s) & 1)) ok = wait_bar(&bar[G::B_O_EMPTY + s], ((tile_phase >> s) & 1) ^ 1, ab, 13);
+                        ok = ok && wait_bar(&bar[G::B_P + s], (block_phase >> s) & 1, ab, 5);
+                        if (!ok) continue;
+                        block_phase ^= 1u << s;
+                    } else {
+                        ok = wait_bar(&bar[G::B_Q + s], (tile_phase >> s) & 1, ab, 3);
+                        if (!ok) continue;
                     }
-                    if (j == n - 1) mma_commit(&bar[G::B_O + s]);
-                    if (j + 1 < n) {
-                        ok = full(2 * j + 2);
-                        if (!ok) break;
-                        product_s(s, j + 1);
+                    tc_fence_after();
+                    if (leader) {
+                        if (j >= 0) {
+#pragma unroll
+                            for (int kk = 0; kk < kBlock / 16; ++kk)
+                                mma_ts(to, ts + kk * 8, bv + (uint64_t)((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                            if (j == n - 1) mma_commit(&bar[G::B_O + s]);
+                        }
+                        if (j + 1 < n) {
+                            const uint64_t a = sdesc_sw128(sb + G::OFF_Q + s * G::TILE, 16, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk >> 2) * G::BOXB + (kk & 3) * 32) >> 4;
+                                mma_ss(ts, a + off, bk + off, ID_S, kk > 0);
+                            }
+                            mma_commit(&bar[G::B_S + s]);
+                            if (j + 2 == n) mma_commit(&bar[G::B_Q_EMPTY + s]);
+                        }
+                    }
+                    __syncwarp();
+                    if (j == n - 1) {
+                        tile_phase ^= 1u << s;
+                        had |= 1u << s;
                     }
                 }
                 if (!ok) break;
-                mma_commit(&bar[G::B_KV_EMPTY + st_v]);
-                if (j + 1 < nb) mma_commit(&bar[G::B_KV_EMPTY + st_k]);
+                if (leader) {
+                    if (j >= 0) mma_commit(&bar[G::B_KV_EMPTY + sv]);
+                    if (j + 1 < nb) mma_commit(&bar[G::B_KV_EMPTY + sk]);
+                }
+                __syncwarp();
+                sv = sk + 1 == G::NST ? 0 : sk + 1;
+                sk = sv + 1 == G::NST ? 0 : sv + 1;
             }
-            // every product issued has completed before TMEM is freed
-            volatile int never = 0;
-            AbortCtx timed{&never, nullptr, kDrainLimitNs};
+            it0 += 2 * nb;
+        }
+        // every product issued has completed before TMEM is freed
+        volatile int never = 0;
+        AbortCtx timed{&never, nullptr, kDrainLimitNs};
+        __syncwarp();
+        if (leader) {
             mma_commit(&bar[G::B_DRAIN]);
             wait_bar(&bar[G::B_DRAIN], 0, timed, 0);
         }
+        __syncwarp();
     } else if (warp == G::SCRUB_WARP) {
-        for (int b = 0; b < n_diag; ++b) {
-            const int j = n0 - 1 + b, i = 2 * j + 1;
-            if (!wait_bar(&bar[G::B_VD + b], 0, ab, 6)) break;
-            const int n = t.end - (t.begin + j * kBlock);   // rows of the sequence
-            if (scrub_values<InT, G::TILE>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane) && lane == 0) flag[b] = 1;
-            fence_proxy_async_smem();
+        int it0 = 0, diag = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Work w = next_work(k);
+            if (w.head < 0) break;
+            const int n0 = blocks0(w), n1 = blocks1(w, n0);
+            for (int b = 0; b < (n1 > n0 ? 2 : 1); ++b, ++diag) {
+                const int j = n0 - 1 + b, i = it0 + 2 * j + 1;
+                ok = wait_bar(&bar[G::B_VD + (diag & 3)], (diag >> 2) & 1, ab, 6);
+                if (!ok) break;
+                const int n = w.end - (w.begin + j * kBlock);   // rows of the sequence
+                const bool bad = scrub_values<InT, G::TILE>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane);
+                if (lane == 0) flag[(k & 3) * 2 + b] = bad;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[G::B_CLEAN + (diag & 3)]);
+            }
+            it0 += 2 * max(n0, n1);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[G::B_CLEAN + b]);
+            if (lane == 0) mbar_arrive(&bar[G::B_WORK_EMPTY + (k & 3)]);
         }
     }
     } else {
         if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // softmax of slot s: thread = row
         const int s = warp >> 2, q = warp & 3;
-        const int n = s ? n1 : n0;
-        const int q0 = PAIR ? t.q0 : t.q0 + s * kBlock;
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const uint32_t t_s = tmem + lane_base + G::T_S + 128 * s, t_o = tmem + lane_base + G::T_O + 128 * s;
         const int r = q * 32 + lane;
         const float c = p.scale_log2;
-        float m = -INFINITY, l = 0.f;
+        int nt = 0, np = 0;   // this slot's tiles and blocks so far
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = wait_bar(&bar[G::B_S + s], j & 1, ab, 7);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t u[4][32];
+        for (int k = 0; ok; ++k) {
+            const Work w = next_work(k);
+            if (w.head < 0) break;
+            const int n0 = blocks0(w), n1 = blocks1(w, n0), n = s ? n1 : n0;
+            const int q0 = MODE == kTwoTiles ? w.q0 + s * kBlock : w.q0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++np) {
+                ok = wait_bar(&bar[G::B_S + s], np & 1, ab, 7);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t u[4][32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, u[i]);
-            tmem_ld_wait();
-            if (j == n - 1) {
-                // diagonal block: keys up to the row's own and within the sequence
-                // (rows behind the sequence see its last key: their results are dropped)
-                const int last = min(r, t.end - 1 - q0);
+                for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, u[i]);
+                tmem_ld_wait();
+                if (j == n - 1) {
+                    // diagonal block: keys up to the row's own and within the sequence
+                    // (rows behind the sequence see its last key: their results are dropped)
+                    const int last = min(r, w.end - 1 - q0);
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > last) u[i / 32][i % 32] = 0xff800000u;
-            }
-            float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+                    for (int i = 0; i < 128; ++i)
+                        if (i > last) u[i / 32][i % 32] = 0xff800000u;
+                }
+                float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i / 32][i % 32]));
-            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (j == 0) {
-                m = mn;
-            } else {
-                const bool move = (mn - m) * c > kLazyLog2;   // (m = -inf: infinite; mn = -inf: NaN, false)
-                if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? ex2_approx((m - mn) * c) : 1.f;
+                for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i / 32][i % 32]));
+                const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (j == 0) {
+                    m = mn;
+                } else {
+                    const bool move = (mn - m) * c > kLazyLog2;   // (m = -inf: infinite; mn = -inf: NaN, false)
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float f = move ? ex2_approx((m - mn) * c) : 1.f;
 #pragma unroll 1
-                    for (int cb = 0; cb < D / 32; ++cb) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + cb * 32, o);
-                        tmem_ld_wait();
+                        for (int cb = 0; cb < D / 32; ++cb) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + cb * 32, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(t_o + cb * 32, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(t_o + cb * 32, o);
+                        }
+                        l *= f;
+                        m = move ? mn : m;
                     }
-                    l *= f;
-                    m = move ? mn : m;
                 }
+                const float neg = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t c2 = pack2(c, c), n2 = pack2(neg, neg);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int e = g * 64 + 2 * i;
+                        float a, b;
+                        unpack2(fma2(pack2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])), c2, n2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+                        pw[i] = pack16<InT>(a, b);
+                    }
+                    tmem_st32(t_s + 32 * g, pw);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[G::B_P + s]);
+                float s0, s1, s2, s3;
+                unpack2(sum[0], s0, s1);
+                unpack2(sum[1], s2, s3);
+                l += (s0 + s1) + (s2 + s3);
             }
-            const float neg = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t c2 = pack2(c, c), n2 = pack2(neg, neg);
-            uint64_t sum[2] = {0ull, 0ull};
+            if (!ok) break;
+            if (n > 0) {
+                ok = wait_bar(&bar[G::B_O + s], nt & 1, ab, 8);
+                if (!ok) break;
+                ++nt;
+                tc_fence_after();
+                const int row = q0 + r;
+                for (int b = 0; b < (n1 > n0 ? 2 : 1); ++b)
+                    if (flag[(k & 3) * 2 + b]) {
+                        const int j0 = w.begin + (n0 - 1 + b) * kBlock;
+                        restore_nonfinite<InT, D>(t_o, v_gmem + (w.head / p.group) * v_hs, v_ts, j0, min(j0 + kBlock, w.end), row);
+                    }
+                // O / l, from the registers to the thread's own row (whole 32-byte
+                // sectors; the query tile is already being filled for the next tile)
+                const float inv = 1.f / l;
+                OutT *out = (OutT *)p.out + (long)(MODE == kTwoHeads ? w.head + s : w.head) * p.o_hs + (long)row * p.o_ts;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = g * 64 + 2 * i;
-                    float a, b;
-                    unpack2(fma2(pack2(__uint_as_float(u[e / 32][e % 32]), __uint_as_float(u[e / 32][e % 32 + 1])), c2, n2), a, b);
-                    a = ex2_approx(a);
-                    b = ex2_approx(b);
-                    sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-                    w[i] = pack16<InT>(a, b);
-                }
-                tmem_st32(t_s + 32 * g, w);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[G::B_P + s]);
-            float s0, s1, s2, s3;
-            unpack2(sum[0], s0, s1);
-            unpack2(sum[1], s2, s3);
-            l += (s0 + s1) + (s2 + s3);
-        }
-        if (ok && n > 0) ok = wait_bar(&bar[G::B_O + s], 0, ab, 8);
-        if (ok && n > 0) {
-            tc_fence_after();
-            const int row = q0 + r;
-            for (int b = 0; b < n_diag; ++b)
-                if (flag[b]) {
-                    const int j0 = t.begin + (n0 - 1 + b) * kBlock;
-                    restore_nonfinite<InT, D>(t_o, v_gmem + hk * v_hs, v_ts, j0, min(j0 + kBlock, t.end), row);
-                }
-            // O / l through this warp's rows of the slot's query tile (no product
-            // reads it any more) to whole-row stores
-            const float inv = 1.f / l;
-            constexpr int RB = D * 2, CPR = RB / 16;        // bytes, 16-byte chunks of a staged row
-            constexpr int PASS = sizeof(OutT) == 4 ? 2 : 1;
-            uint8_t *stg = smem + G::OFF_Q + s * G::TILE + q * 32 * RB;
-            OutT *out = (OutT *)p.out + (long)(PAIR ? h0 + s : h0) * p.o_hs;
-#pragma unroll 1
-            for (int ps = 0; ps < PASS; ++ps) {
-#pragma unroll
-                for (int cb = 0; cb < D / 32 / PASS; ++cb) {
+                for (int cb = 0; cb < D / 32; ++cb) {
                     uint32_t o[32];
-                    tmem_ld32(t_o + ps * (D / 2) + cb * 32, o);
+                    __syncwarp();
+                    tmem_ld32(t_o + cb * 32, o);
                     tmem_ld_wait();
+                    if (cb == D / 32 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[G::B_O_EMPTY + s]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if constexpr (PASS == 1) {
+                    if (row >= w.end) {
+                        // behind the sequence: not a row of it
+                    } else if constexpr (sizeof(OutT) == 2) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            uint4 w;
-                            uint32_t *wp = reinterpret_cast<uint32_t *>(&w);
+                            uint4 v;
+                            uint32_t *vp = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                wp[y] = pack16<InT>(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
-                            *reinterpret_cast<uint4 *>(stg + lane * RB + (((cb * 4 + x) ^ (lane & 7)) << 4)) = w;
+                                vp[y] = pack16<InT>(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
+                            reinterpret_cast<uint4 *>(out + cb * 32)[x] = v;
                         }
                     } else {
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            *reinterpret_cast<uint4 *>(stg + lane * RB + (((cb * 8 + x) ^ (lane & 7)) << 4)) =
-                                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                            reinterpret_cast<uint4 *>(out + cb * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                     }
                 }
-                __syncwarp();
-#pragma unroll 4
-                for (int i = lane; i < 32 * CPR; i += 32) {
-                    const int rr = i / CPR, ch = i % CPR;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(stg + rr * RB + ((ch ^ (rr & 7)) << 4));
-                    const int row_g = q0 + q * 32 + rr;
-                    if (row_g < t.end)
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(out + (long)row_g * p.o_ts) + ps * RB + ch * 16) = w;
-                }
-                __syncwarp();
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[G::B_WORK_EMPTY + (k & 3)]);
         }
     }
     tc_fence_before();
