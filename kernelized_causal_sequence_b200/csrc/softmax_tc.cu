@@ -61,23 +61,20 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long l
                          false, "softmax tensor-core launch", mq, mk, mv, (const InT *)sp.v, sp.v_hs, sp.v_ts, p);
 }
 
-// Which slots (us, 16 query heads, one and two slots; S sequences of L tokens):
-//   d 128, heads shared evenly: two heads read each key/value tile once for
-//     both (16 x 1000: 133 / 119; 1 x 8192: 288 / 246; 64 x 200: 84 / 78)
-//   d 128, else: two tiles of one head, but for short sequences, which leave
-//     the second empty (256 x 64: 139 / 212; 64 x 256: 93 / 96; 32 x 512: 108 / 105)
-//   d 64: the tiles are half as large and the exponentials bound it; two CTAs
-//     of one slot overlap each other's start and end (16 x 1000: 99 / 112;
-//     1 x 8192: 226 / 233), but for long sequences with heads shared evenly
-//     (16 x 1000: 98 / 100; 4 x 4096: 242 / 237)
+// Which slots (us, 16 query heads; one tile / two slots; S sequences of L tokens):
+//   d 128, 4 key heads   64 x 200: 63 / 67, 16 x 1000: 112 / 113, 8 x 2048: 166 / 161, 1 x 8192: 261 / 250
+//   d 128, 16 key heads  64 x 200: 64 / 73, 16 x 1000: 116 / 122, 8 x 2048: 173 / 171, 1 x 8192: 271 / 259
+//   d 128, 1 x 2048      41 / 45 (too few tiles of two slots)
+//   d 64                 one tile up to 8192 tokens (1 x 8192: 200 / 209): the softmax bounds it there
+// Two slots read a key and value tile once for both, which counts where the
+// products' operands bound it; one tile leaves less empty and more to overlap.
 template <typename InT, typename OutT, int D>
 la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
-    const bool even = sp.group % 2 == 0;
     if constexpr (D == 128) {
-        if (even) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
-        if ((long)sp.N > 384L * sp.n_seq) return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, status, wait_ns, st);
-    } else {
-        if (even && (long)sp.N > 2048L * sp.n_seq) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
+        if ((long)sp.N > 1024L * sp.n_seq && (long)seq_tiles(sp.N, sp.n_seq, 256) * sp.H >= 2L * kNumSMs) {
+            if (sp.group % 2 == 0) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
+            return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, status, wait_ns, st);
+        }
     }
     return run<InT, OutT, D, stc::kOneTile>(sp, dt, status, wait_ns, st);
 }

@@ -25,7 +25,8 @@
 // 1%); they run at what the tensor core gets from shared memory, whose reads
 // for Q K^T (8 KB per 128 x 128 x 16 product) and P V and whose fills together
 // take as long as the products.  At d 64 the products are half as long and the
-// softmax is the bound (226 us with, 170 us without it: 8192 tokens, 16 heads).
+// softmax is the bound (226 us with, 170 us without it when this was tried: 8192
+// tokens, 16 heads; 200 us now).
 // Computing part of the exponentials on the FMA units gained nothing: a warp's
 // issue, not the special-function unit, sets the softmax's pace.
 //
@@ -33,8 +34,8 @@
 // the copies and the first products of the next tile run during the softmax and
 // the output of the last.
 //
-// Warps (S = 4 per slot softmax warps, then):
-//   softmax    a thread owns one row (TMEM lane)
+// Warps (four per slot for the softmax, S in all, then three):
+//   0 .. S - 1 softmax: a thread owns one row (TMEM lane)
 //   S          the list and the TMA copies (one thread): K_0, Q, V_0, K_1, ...
 //   S + 1      TMEM allocation, MMA issue (one thread)
 //   S + 2      the values of a diagonal block: rows behind the sequence are
@@ -73,7 +74,8 @@ template <int D, int MODE> struct Cfg {
     static constexpr int BOXB = kBlock * 128;
     static constexpr int TILE = kBlock * D * 2;
     // K and V tiles in flight: all the shared memory there is
-    static constexpr int NST = SLOTS == 1 ? (D == 128 ? 2 : 5) : (D == 128 ? 5 : 8);
+    static constexpr int NST = SLOTS == 2 ? 5 : D == 128 ? 2 : 5;
+    static_assert(D == 128 || SLOTS == 1, "two slots: d 128 only");
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_KV = SLOTS * TILE;
     static constexpr int OFF_BAR = OFF_KV + NST * TILE;
@@ -202,13 +204,6 @@ __device__ __forceinline__ void restore_nonfinite(uint32_t t_o, const InT *v, lo
     tmem_st_wait();
 }
 
-// The one thread of a warp that issues for it.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // mbar_wait without a call: a kernel that redistributes its registers may not
 // call functions.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const AbortCtx &ab, int code) {
@@ -223,6 +218,18 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const A
         }
     }
     return true;
+}
+
+// The same by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const AbortCtx &ab, int code) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, ab, code));
+}
+
+// The one thread of a warp that issues for it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <typename InT, typename OutT, int D, int MODE>
@@ -266,10 +273,10 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto blocks1 = [&](const Work &w, int n0) {
         return MODE == kTwoHeads ? n0 : MODE == kTwoTiles && w.q0 + kBlock < w.end ? n0 + 1 : 0;
     };
-    // Entry k of the list, or head < 0 (the end, or giving up).
-    auto next_work = [&](int k) {
+    // Entry k of the list once its wait is over, or head < 0 (the end, or giving up).
+    auto next_work = [&](int k, bool ready) {
         Work w{0, 0, 0, -1};
-        if (wait_bar(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10)) {
+        if (ready) {
             w.begin = work[k & 3].begin;
             w.end = work[k & 3].end;
             w.q0 = work[k & 3].q0;
@@ -356,7 +363,8 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     } else if (warp == G::MMA_WARP) {
         // The whole warp goes through the waits and the index arithmetic, so that
         // the descriptors are uniform values, ready before the last wait; one
-        // thread issues the products and the commits.
+        // thread issues the products and the commits.  (No vote on the waits: a lane
+        // that gives up goes to the end, and nothing here needs the others with it.)
         constexpr bool BF = std::is_same<InT, bf16>::value;
         constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
         constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
@@ -372,9 +380,8 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             return f;
         };
         for (int k = 0; ok; ++k) {
-            const Work w = next_work(k);
+            const Work w = next_work(k, wait_bar(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10));
             if (w.head < 0) break;
-            __syncwarp();
             if (leader) mbar_arrive(&bar[G::B_WORK_EMPTY + (k & 3)]);
             const int n0 = blocks0(w), n1 = blocks1(w, n0), nb = max(n0, n1);
             // step j: per slot P V_j, then S of block j + 1
@@ -424,7 +431,6 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             if (j + 2 == n) mma_commit(&bar[G::B_Q_EMPTY + s]);
                         }
                     }
-                    __syncwarp();
                     if (j == n - 1) {
                         tile_phase ^= 1u << s;
                         had |= 1u << s;
@@ -435,7 +441,6 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     if (j >= 0) mma_commit(&bar[G::B_KV_EMPTY + sv]);
                     if (j + 1 < nb) mma_commit(&bar[G::B_KV_EMPTY + sk]);
                 }
-                __syncwarp();
                 sv = sk + 1 == G::NST ? 0 : sk + 1;
                 sk = sv + 1 == G::NST ? 0 : sv + 1;
             }
@@ -454,12 +459,12 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         int it0 = 0, diag = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            const Work w = next_work(k);
+            const Work w = next_work(k, wait_warp(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10));
             if (w.head < 0) break;
             const int n0 = blocks0(w), n1 = blocks1(w, n0);
             for (int b = 0; b < (n1 > n0 ? 2 : 1); ++b, ++diag) {
                 const int j = n0 - 1 + b, i = it0 + 2 * j + 1;
-                ok = wait_bar(&bar[G::B_VD + (diag & 3)], (diag >> 2) & 1, ab, 6);
+                ok = wait_warp(&bar[G::B_VD + (diag & 3)], (diag >> 2) & 1, ab, 6);
                 if (!ok) break;
                 const int n = w.end - (w.begin + j * kBlock);   // rows of the sequence
                 const bool bad = scrub_values<InT, G::TILE>(smem + G::OFF_KV + (i % G::NST) * G::TILE, n, lane);
@@ -484,13 +489,13 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         int nt = 0, np = 0;   // this slot's tiles and blocks so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            const Work w = next_work(k);
+            const Work w = next_work(k, wait_warp(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10));
             if (w.head < 0) break;
             const int n0 = blocks0(w), n1 = blocks1(w, n0), n = s ? n1 : n0;
             const int q0 = MODE == kTwoTiles ? w.q0 + s * kBlock : w.q0;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j, ++np) {
-                ok = wait_bar(&bar[G::B_S + s], np & 1, ab, 7);
+                ok = wait_warp(&bar[G::B_S + s], np & 1, ab, 7);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t u[4][32];
@@ -557,7 +562,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             if (!ok) break;
             if (n > 0) {
-                ok = wait_bar(&bar[G::B_O + s], nt & 1, ab, 8);
+                ok = wait_warp(&bar[G::B_O + s], nt & 1, ab, 8);
                 if (!ok) break;
                 ++nt;
                 tc_fence_after();

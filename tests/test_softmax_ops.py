@@ -157,9 +157,11 @@ PREFILL = [
     (torch.float16, None, 64, 8, 1, [1, 300, 0, 0, 511], 0),
     (torch.float16, torch.float32, 128, 2, 2, [1000, 24], 0),
     (torch.float16, None, 128, 3, 1, [2049], 1),
-    # each way the tensor-core kernel fills a CTA, at d 64 and 128: two heads, two tiles, one tile
+    # each way the tensor-core kernel fills a CTA: one tile, two heads, two tiles
     (torch.bfloat16, None, 64, 4, 2, [2500, 2100], 1),
     (torch.float16, torch.float32, 64, 2, 1, [2305], 0),
+    (torch.bfloat16, None, 128, 32, 16, [2500, 130], 7),
+    (torch.float16, torch.float32, 128, 30, 2, [1, 3000], 0),
     (torch.bfloat16, None, 128, 3, 3, [1, 130, 77, 0, 256, 383, 300], 65),
     (torch.float16, torch.float32, 128, 1, 1, [255, 129, 128, 1], 0),
     (torch.bfloat16, torch.float32, 128, 3, 1, [700, 384, 900], 3),
@@ -216,8 +218,7 @@ def test_prefill_hidden_keys_do_not_reach(la, dtype, d, bad):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("H,Hkv,first", [(3, 3, 300), (3, 3, 900), (4, 2, 5000)])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,first,d", [(3, 3, 300, 64), (3, 3, 300, 128), (32, 16, 2900, 128), (30, 2, 2900, 128)])
 def test_prefill_hidden_keys_all_slots(la, H, Hkv, first, d):
     """The same where a CTA holds one tile, two tiles and two heads."""
     hidden_keys(la, torch.bfloat16, d, H, Hkv, math.nan, first=first)
@@ -632,3 +633,24 @@ def test_serving_run(la, dtype, d, H, Hkv):
         tol = tol + (U[dtype] if dtype != torch.float32 else 2.0 ** -16) * A
         tol = tol + U[dtype] * (ref.abs() + tol)
         assert float(((o2[s].double().cpu() - ref[0]).abs() / tol[0]).max()) <= 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,d,n", [(4, 2, 64, 700), (4, 2, 128, 700), (32, 16, 128, 2500)])
+def test_prefill_wait_limit(la, H, Hkv, d, n):
+    """With a wait limit of 0 the kernel gives up and says so in the status
+    word; the next call, with the limit back, is right."""
+    q, k, v = (x.to(DEV) for x in prefill_inputs(torch.bfloat16, d, H, Hkv, n, seed=31))
+    cu = cu_of([n])
+    ws = torch.empty(la.la_softmax_prefill_workspace_size(H, Hkv, n, d, 1), dtype=torch.uint8, device=DEV)
+    want = la.la_softmax_prefill(q, k, v, cu, workspace=ws)
+    assert la.la_workspace_status(ws) == (la.LA_OK, 0)
+    old = la.la_set_wait_limit_ns(0)
+    try:
+        la.la_softmax_prefill(q, k, v, cu, workspace=ws)
+        status, waiter = la.la_workspace_status(ws)
+    finally:
+        la.la_set_wait_limit_ns(old)
+    assert status == la.LA_ERR_TIMEOUT and waiter > 0
+    assert torch.equal(la.la_softmax_prefill(q, k, v, cu, workspace=ws), want)
+    assert la.la_workspace_status(ws) == (la.LA_OK, 0)
