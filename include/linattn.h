@@ -348,9 +348,8 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  *   out    must not overlap the inputs
  * Keys and values behind a query, or of another sequence, do not reach it,
  * not even as NaN or infinity.  Sums and the running maximum are fp32; with
- * 16-bit inputs at d 64 or 128 (the tensor-core kernel) the unnormalised
- * weights, which lie in [0, 256], are rounded once to the input type for the
- * product with v.
+ * 16-bit inputs (the tensor-core kernel) the unnormalised weights, which lie
+ * in [0, 256], are rounded once to the input type for the product with v.
  * The workspace (la_softmax_prefill_workspace_size bytes, 256-byte aligned)
  * starts with the status word that la_workspace_status reads.
  */
@@ -423,10 +422,10 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
  *           weights_in (zeros if NULL) + the sum of p_t over the query heads
  *           of that key/value head; the other entries are left as they were.
  *           May be weights_in itself; must not overlap it otherwise.
- * The products run on the tensor cores in 16-bit terms: 4-bit codes are exact
- * there, 16-bit queries too; fp32 queries are carried as three bf16 terms and
- * the weights times the values' scales as one term of the query's type
- * (fp32: two bf16 terms).  Sums are fp32.
+ * The products run on the tensor cores in fp16 terms, scaled by powers of two:
+ * 4-bit codes and 16-bit queries are exact there; the weights times the
+ * values' scales are rounded once to fp16's 11 bits (16-bit queries) or carried
+ * as two terms, like fp32 queries.  Sums are fp32.
  */
 la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_cache *cache, const int32_t *lens,
                         float scale, const float *weights_in, float *weights_out, void *out,

@@ -109,17 +109,15 @@ inline unsigned stride_grid(long items, int per, long others) {
     if (out == LA_F16) { using InT = f16; using OutT = f16; CALL; }                         \
     { using InT = f16; using OutT = float; CALL; }
 
-template <typename InT, typename OutT, int BM>
-la_status run_softmax_simt_bm(const SoftmaxParams &p, int d, cudaStream_t st) {
-    LA_BY_D(d, return launch_kernel(softmax_simt_kernel<InT, OutT, D, BM>,
+template <int BM> la_status run_softmax_simt_bm(const SoftmaxParams &p, int d, cudaStream_t st) {
+    LA_BY_D(d, return launch_kernel(softmax_simt_kernel<D, BM>,
                                     dim3((unsigned)seq_tiles(p.N, p.n_seq, BM), (unsigned)p.H), dim3(kSsThreads),
                                     softmax_simt_smem<D, BM>(), st, true, "softmax prefill launch", p))
 }
-template <typename InT, typename OutT>
 la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
     // tiles of 64 queries fill the machine, or tiles of 16 for more CTAs
-    if ((long)seq_tiles(p.N, p.n_seq, 64) * p.H >= kNumSMs) return run_softmax_simt_bm<InT, OutT, 64>(p, d, st);
-    return run_softmax_simt_bm<InT, OutT, 16>(p, d, st);
+    if ((long)seq_tiles(p.N, p.n_seq, 64) * p.H >= kNumSMs) return run_softmax_simt_bm<64>(p, d, st);
+    return run_softmax_simt_bm<16>(p, d, st);
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {
     const dim3 grid((unsigned)((p.N + kAppendThreads / 8 - 1) / (kAppendThreads / 8)), (unsigned)p.c.Hkv, 2);
@@ -223,12 +221,12 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
     p.H = H; p.group = H / H_kv; p.N = N; p.n_seq = n_seq;
     p.scale_log2 = scale * kLog2e;
     p.status = (int *)workspace;
-    if (softmax_tc_supported(in_dtype, d)) {
+    if (softmax_tc_supported(in_dtype)) {
         // the status word and the tile counter behind it
         if ((s = cuda_check("status memset", cudaMemsetAsync(workspace, 0, 4 * sizeof(int), st))) != LA_OK) return s;
         return softmax_tc(p, in_dtype, out_dtype, d, (int *)workspace, wait_limit_ns(), st);
     }
-    LA_BY_TYPES(in_dtype, out_dtype, return (run_softmax_simt<InT, OutT>(p, d, st)))
+    return run_softmax_simt(p, d, st);
 }
 
 la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, const int64_t *strides,

@@ -1,6 +1,6 @@
 // softmax_simt.cuh — causal softmax attention over packed sequences on the
-// CUDA cores: fp32 inputs (whose 1e-4 class the 16-bit tensor-core operands
-// cannot meet) and head dim 32.
+// CUDA cores, for fp32 inputs (whose 1e-4 class the 16-bit tensor-core operands
+// cannot meet).
 //
 // One CTA takes BM queries of one head (64, or 16 where 64 would leave most SMs
 // without work) and walks the keys up to its last query in tiles of 64, keeping
@@ -61,7 +61,7 @@ template <int N> __device__ __forceinline__ void lds_rows(const float *p, float 
     }
 }
 
-template <typename InT, typename OutT, int D, int BM>
+template <int D, int BM>
 __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams p) {
     constexpr int CT = D / 16;                           // output channels per thread
     constexpr int RW = BM / 16;                          // rows per thread
@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
     const SeqTile t = seq_tile<BM>(p.cu, p.n_seq, p.N, blockIdx.x);
     if (t.q0 >= t.end) return;
     const int h = blockIdx.y, hk = h / p.group;
-    const InT *Q = (const InT *)p.q + h * p.q_hs;
-    const InT *K = (const InT *)p.k + hk * p.k_hs;
-    const InT *V = (const InT *)p.v + hk * p.v_hs;
+    const float *Q = (const float *)p.q + h * p.q_hs;
+    const float *K = (const float *)p.k + hk * p.k_hs;
+    const float *V = (const float *)p.v + hk * p.v_hs;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     // keys: thread = row (conflict-free transposed stores); values: thread = piece of a row
     float4 kr[NL], vr[NL];
@@ -89,15 +89,15 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
             const int kj = j0 + tid % kSsTile, kc = (tid / kSsTile + i * (kSsThreads / kSsTile)) * 4;
             const int x = tid + i * kSsThreads, vj = j0 + x / (D / 4), vc = (x % (D / 4)) * 4;
             kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (kj < t.end) kr[i] = load4<InT>(K + (long)kj * p.k_ts + kc);
-            if (vj < t.end) vr[i] = load4<InT>(V + (long)vj * p.v_ts + vc);
+            if (kj < t.end) kr[i] = load4<float>(K + (long)kj * p.k_ts + kc);
+            if (vj < t.end) vr[i] = load4<float>(V + (long)vj * p.v_ts + vc);
         }
     };
     load(t.begin);
     for (int x = tid; x < BM * (D / 4); x += kSsThreads) {
         const int r = x % BM, c = (x / BM) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t.q0 + r < t.end) v = load4<InT>(Q + (long)(t.q0 + r) * p.q_ts + c);
+        if (t.q0 + r < t.end) v = load4<float>(Q + (long)(t.q0 + r) * p.q_ts + c);
         qs[(c + 0) * QP + r] = v.x;
         qs[(c + 1) * QP + r] = v.y;
         qs[(c + 2) * QP + r] = v.z;
@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
     for (int i = 0; i < RW; ++i) {
         const int r = t.q0 + ty * RW + i;
         if (r < t.end) {
-            OutT *dst = (OutT *)p.out + h * p.o_hs + (long)r * p.o_ts + tx;
+            float *dst = (float *)p.out + h * p.o_hs + (long)r * p.o_ts + tx;
             const float inv = 1.f / l[i];
 #pragma unroll
-            for (int c = 0; c < CT; ++c) dst[c * 16] = from_f32<OutT>(o[i][c] * inv);
+            for (int c = 0; c < CT; ++c) dst[c * 16] = o[i][c] * inv;
         }
     }
 }

@@ -26,7 +26,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode() {
 }
 
 // [heads][N][d] with strides, boxes of 64 channels x 128 rows, 128-byte
-// swizzle, zeros past N
+// swizzle, zeros past N and past d
 bool map16(CUtensorMap *m, const void *base, la_dtype dt, int heads, int N, int d, long hs, long ts) {
     auto enc = encode();
     if (!enc) return false;
@@ -41,17 +41,17 @@ bool map16(CUtensorMap *m, const void *base, la_dtype dt, int heads, int N, int 
 }
 
 template <typename InT, typename OutT, int D, int MODE>
-la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
+la_status run(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     const int Hk = sp.H / sp.group;
-    if (!map16(&mq, sp.q, dt, sp.H, sp.N, D, sp.q_hs, sp.q_ts) || !map16(&mk, sp.k, dt, Hk, sp.N, D, sp.k_hs, sp.k_ts) ||
-        !map16(&mv, sp.v, dt, Hk, sp.N, D, sp.v_hs, sp.v_ts))
+    if (!map16(&mq, sp.q, dt, sp.H, sp.N, d, sp.q_hs, sp.q_ts) || !map16(&mk, sp.k, dt, Hk, sp.N, d, sp.k_hs, sp.k_ts) ||
+        !map16(&mv, sp.v, dt, Hk, sp.N, d, sp.v_hs, sp.v_ts))
         return cuda_fail_msg("cuTensorMapEncodeTiled", "tensor map encoding failed");
     stc::Params p;
     p.out = sp.out; p.cu = sp.cu; p.o_hs = sp.o_hs; p.o_ts = sp.o_ts;
     p.H = sp.H; p.group = sp.group; p.N = sp.N; p.n_seq = sp.n_seq;
     p.tiles = seq_tiles(sp.N, sp.n_seq, MODE == stc::kTwoTiles ? 256 : 128);
-    p.scale_log2 = sp.scale_log2; p.status = status; p.wait_ns = wait_ns;
+    p.cols = d; p.scale_log2 = sp.scale_log2; p.status = status; p.wait_ns = wait_ns;
     const long tiles = (long)p.tiles * (MODE == stc::kTwoHeads ? sp.H / 2 : sp.H);
     if (tiles > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
     using G = stc::Cfg<D, MODE>;
@@ -69,19 +69,20 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long l
 // Two slots read a key and value tile once for both, which counts where the
 // products' operands bound it; one tile leaves less empty and more to overlap.
 template <typename InT, typename OutT, int D>
-la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int *status, unsigned long long wait_ns, cudaStream_t st) {
+la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
     if constexpr (D == 128) {
         if ((long)sp.N > 1024L * sp.n_seq && (long)seq_tiles(sp.N, sp.n_seq, 256) * sp.H >= 2L * kNumSMs) {
-            if (sp.group % 2 == 0) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, status, wait_ns, st);
-            return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, status, wait_ns, st);
+            if (sp.group % 2 == 0) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, d, status, wait_ns, st);
+            return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, d, status, wait_ns, st);
         }
     }
-    return run<InT, OutT, D, stc::kOneTile>(sp, dt, status, wait_ns, st);
+    return run<InT, OutT, D, stc::kOneTile>(sp, dt, d, status, wait_ns, st);
 }
 
 template <typename InT, typename OutT>
 la_status by_shape(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
-    return d == 128 ? by_slots<InT, OutT, 128>(sp, dt, status, wait_ns, st) : by_slots<InT, OutT, 64>(sp, dt, status, wait_ns, st);
+    return d == 128 ? by_slots<InT, OutT, 128>(sp, dt, d, status, wait_ns, st)
+                    : by_slots<InT, OutT, 64>(sp, dt, d, status, wait_ns, st);
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // softmax_tc.cuh — causal softmax attention over packed sequences on the
-// tensor cores (bf16/fp16 inputs, head dim 64 or 128, fp32 sums).
+// tensor cores (bf16/fp16 inputs, head dim 32 as a padded 64, 64 or 128, fp32
+// sums).
 //
 // A CTA holds one or two tiles ("slots") of 128 queries that read the same keys
 // and values (enum Slots), and walks the keys in blocks of 128 from the
@@ -109,6 +110,7 @@ struct Params {
     const int32_t *cu;
     long o_hs, o_ts;
     int H, group, N, n_seq, tiles;
+    int cols;      // the tensors' head dim (32: the copies fill channels 32 .. 63 of a d 64 tile with zeros)
     float scale_log2;
     int *status;   // [0], [1] the status word, [2] the next tile
     unsigned long long wait_ns;
@@ -187,8 +189,8 @@ template <typename InT, int TILE> __device__ __forceinline__ bool scrub_values(u
 // Adds the NaN and infinities of values j0 .. min(j1, row) to this thread's
 // row of O (p > 0 times infinity is infinity).  Rare; whole warp.
 template <typename InT, int D>
-__device__ __forceinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long ts, int j0, int j1, int row) {
-    for (int cb = 0; cb < D / 32; ++cb) {
+__device__ __forceinline__ void restore_nonfinite(uint32_t t_o, const InT *v, long ts, int j0, int j1, int row, int cols) {
+    for (int cb = 0; cb < cols / 32; ++cb) {
         uint32_t u[32];
         tmem_ld32(t_o + cb * 32, u);
         tmem_ld_wait();
@@ -570,7 +572,8 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int b = 0; b < (n1 > n0 ? 2 : 1); ++b)
                     if (flag[(k & 3) * 2 + b]) {
                         const int j0 = w.begin + (n0 - 1 + b) * kBlock;
-                        restore_nonfinite<InT, D>(t_o, v_gmem + (w.head / p.group) * v_hs, v_ts, j0, min(j0 + kBlock, w.end), row);
+                        restore_nonfinite<InT, D>(t_o, v_gmem + (w.head / p.group) * v_hs, v_ts, j0, min(j0 + kBlock, w.end), row,
+                                                  p.cols);
                     }
                 // O / l, from the registers to the thread's own row (whole 32-byte
                 // sectors; the query tile is already being filled for the next tile)
@@ -589,8 +592,8 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if (row >= w.end) {
-                        // behind the sequence: not a row of it
+                    if (row >= w.end || cb * 32 >= p.cols) {
+                        // behind the sequence: not a row of it; behind the channels
                     } else if constexpr (sizeof(OutT) == 2) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {

@@ -150,6 +150,7 @@ PREFILL = [
     (torch.float32, None, 128, 2, 2, [129, 300], 1),
     (torch.bfloat16, None, 32, 4, 4, [70, 2, 129], 0),
     (torch.float16, torch.float32, 32, 2, 1, [257], 9),
+    (torch.float16, None, 32, 6, 2, [1, 128, 129, 0, 1000], 2),
     (torch.bfloat16, None, 128, 4, 1, [1], 0),
     (torch.bfloat16, None, 128, 4, 2, [1, 2, 3, 127, 128, 129, 0, 255, 256, 257], 5),
     (torch.bfloat16, torch.float32, 128, 6, 2, [385, 513], 0),
@@ -179,7 +180,8 @@ def cu_of(lens):
 
 
 def tensor_cores(dtype, d):
-    return dtype != torch.float32 and d in (64, 128)
+    # 16-bit inputs: the weights are rounded to that type
+    return dtype != torch.float32
 
 
 @pytest.mark.gpu
