@@ -351,7 +351,8 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  * 16-bit inputs (the tensor-core kernel) the unnormalised weights, which lie
  * in [0, 256], are rounded once to the input type for the product with v.
  * The workspace (la_softmax_prefill_workspace_size bytes, 256-byte aligned)
- * starts with the status word that la_workspace_status reads.
+ * starts with the status word that la_workspace_status reads.  Calls that may
+ * overlap on the GPU need workspaces of their own (here and below).
  */
 la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dtype in_dtype, int H, int H_kv,
                              int N, int d, const int32_t *cu_seqlens, int n_seq, const int64_t *strides,
@@ -417,7 +418,7 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
  * cache's first lens[b] positions (lens [B] int32, device, clamped to
  * [0, cap]; a length of 0 gives zeros):
  *   out[b,h] = sum_t p_t V[b,h',t],  p = softmax_t(scale q[b,h].K[b,h',t])
- *   q, out  [B, H, d] contiguous
+ *   q, out  [B, H, d] contiguous; out must not overlap q
  *   weights_out  [B, H_kv, cap] fp32 or NULL: for t < lens[b] receives
  *           weights_in (zeros if NULL) + the sum of p_t over the query heads
  *           of that key/value head; the other entries are left as they were.

@@ -374,7 +374,10 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
             lds_words(st + C::OFF_VP + lane * 4 * G, vw);
             uint32_t big = 0u;
 #pragma unroll
-            for (int g = 0; g < G; ++g) big = max(big, vw[g] << 16);
+            for (int g = 0; g < G; ++g) {
+                const uint32_t bits = vw[g] << 16;
+                if (bits < 0x7f800000u) big = max(big, bits);   // (a group of NaN is its own: it sets no unit)
+            }
             // The unit grows with the largest scale met (in [2^e, 2^(e + 1)): p s < 2^8 2^(e + 1) = 2^15 unit);
             // one-term queries sum their products in it from tile to tile.
             if (TILE_SUMS || __any_sync(0xffffffffu, big >= unit_end)) {

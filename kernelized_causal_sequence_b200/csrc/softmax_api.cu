@@ -284,6 +284,8 @@ la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_ca
     if (H == 0 || cache->B == 0) return LA_OK;
     if (!q || !lens || !out || !al16(q) || !al16(out) || !al4(lens) || !al16(weights_in) || !al16(weights_out))
         return LA_ERR_INVALID_ARG;
+    const size_t elems = (size_t)cache->B * H * cache->d;
+    if (overlap(out, elems * esize(out_dtype), q, elems * esize(in_dtype))) return LA_ERR_INVALID_ARG;
     const size_t wb = (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float);
     if (weights_in != weights_out && overlap(weights_in, wb, weights_out, wb)) return LA_ERR_INVALID_ARG;
     const DecodePlan pl = decode_plan(cache->B, H, cache->H_kv, cache->cap, cache->d, weights_out != nullptr);

@@ -115,6 +115,7 @@ def test_decode_refusals(L):
     assert dec(q=None) == dec(lens=None) == dec(out=None) == dec(q=P(1, 4)) == dec(lens=P(2, 2)) == INVALID
     assert dec(dt=9) == dec(H=3) == dec(H=-2) == dec(scale=0.0) == dec(scale=float("nan")) == INVALID
     assert dec(wo=None) == dec(wi=P(5, 4)) == dec(wo=P(6, 8)) == dec(wi=P(6, 16)) == INVALID
+    assert dec(out=P(1)) == dec(out=P(1, 16)) == INVALID
     assert dec(ws=None) == dec(nws=need - 1) == dec(ws=P(4, 16)) == INVALID
     assert dec(odt=2) == dec(H=70000) == UNSUPPORTED
     assert la.la_kv4_decode_workspace_size(3, 5, 2, 100, 64) == 0

@@ -501,6 +501,45 @@ def test_decode_peaked_and_flat(la):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H", [(torch.bfloat16, 4), (torch.float32, 4), (torch.float16, 12)])
+@pytest.mark.parametrize("T", [50, 900])
+def test_decode_nan_values_stay_in_their_group(la, dtype, H, T):
+    """A value group of NaN reaches its 32 channels of the output and no others."""
+    d = 128
+    g = torch.Generator().manual_seed(12)
+    k, v = torch.randn(2, 1, T, d, generator=g), torch.randn(2, 1, T, d, generator=g)
+    q = torch.randn(2, H, d, generator=g).to(dtype).to(DEV)
+    cache, _, _ = fill_cache(la, k, v)
+    tl = torch.tensor([T, T], dtype=torch.int32, device=DEV)
+    clean = la.la_kv4_decode(q, cache, tl)
+    cache.v_par[1, 0, T // 2, 2] = 0x7fc0
+    got = la.la_kv4_decode(q, cache, tl)
+    assert torch.isnan(got[1, :, 64:96]).all()
+    same = torch.ones_like(clean, dtype=torch.bool)
+    same[1, :, 64:96] = False
+    # (the NaN scale may have been the largest of its tile, by which the others' are held)
+    assert torch.allclose(got[same].float(), clean[same].float(), rtol=2 * U[dtype], atol=1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("mag", [1e-30, 1e-6, 1e30])
+def test_decode_value_magnitudes(la, dtype, mag):
+    """Values far below and above 16-bit products' range, and growing by 2^12 along the cache."""
+    T, d = 600, 64
+    g = torch.Generator().manual_seed(13)
+    k = torch.randn(1, 2, T, d, generator=g)
+    v = torch.randn(1, 2, T, d, generator=g) * mag * torch.logspace(0, 12, T, base=2.0)[:, None]
+    q = torch.randn(1, 4, d, generator=g).to(dtype)
+    cache, kv, vv = fill_cache(la, k, v)
+    ref, tol, A, _, _ = ref_decode(q, kv, vv, [T], d ** -0.5, torch.from_numpy(pack_ref(v)[1]))
+    out = la.la_kv4_decode(q.to(DEV), cache, torch.tensor([T], dtype=torch.int32, device=DEV), out_dtype=torch.float32)
+    tol = tol + (U[torch.float16] if dtype != torch.float32 else 2.0 ** -16) * A
+    tol = tol + U32 * (ref.abs() + tol)
+    assert float(((out.double().cpu() - ref).abs() / tol).max()) <= 1.0
+
+
+@pytest.mark.gpu
 def test_decode_lengths_are_clamped(la):
     T, d = 100, 64
     g = torch.Generator().manual_seed(11)
@@ -532,6 +571,9 @@ EVICT = [
     (128, 3, 5000, [5000, 4097, 12], 1000, 128),
     (128, 1, 20000, [20000], 19999, 5),
     (32, 1, 20000, [19000], 1, 0),
+    # slices that do not fit a block's registers: of one CTA, of a cluster
+    (32, 2, 9000, [9000, 8500] + [5] * 73, 100, 7),
+    (32, 1, 70000, [70000], 30000, 10),
 ]
 
 
