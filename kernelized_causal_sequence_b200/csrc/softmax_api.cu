@@ -333,6 +333,11 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     if (overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), out_weights,
                 (size_t)out->B * out->H_kv * out->cap * sizeof(float)))
         return LA_ERR_INVALID_ARG;
+    // (a head's lengths are read while another's results are written)
+    const size_t lb = sizeof(int32_t) * (size_t)cache->B, kb = (size_t)cache->B * cache->H_kv * keep * sizeof(int32_t);
+    if (overlap(lens, lb, out_lens, lb) || overlap(lens, lb, kept, kb) ||
+        overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), kept, kb))
+        return LA_ERR_INVALID_ARG;
     // the list of kept positions: the caller's `kept`, or the workspace
     const size_t need = kept ? 0 : ws_up((size_t)cache->B * cache->H_kv * keep * sizeof(int32_t));
     if (!ws_ok(workspace, workspace_bytes, need)) return LA_ERR_INVALID_ARG;

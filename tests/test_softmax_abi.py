@@ -136,6 +136,14 @@ def test_evict_refusals(L):
     assert ev(kept=None, ws=None) == ev(kept=None, nws=need - 1) == ev(kept=None, ws=P(3, 32)) == INVALID
 
 
+def test_evict_refuses_outputs_over_inputs(L):
+    """One head's results are written while another's lengths and weights are read."""
+    def ev(lens=P(2), kept=P(6), ol=P(7)):
+        return L.la_kv4_evict(ctypes.byref(cache()), P(1), lens, 10, 0, ctypes.byref(cache(20, cap=12)), P(5), kept, ol,
+                              None, 0, None)
+    assert ev(ol=P(2)) == ev(lens=P(2, 8), ol=P(2)) == ev(kept=P(2)) == ev(kept=P(1, 16)) == INVALID
+
+
 def test_python_checks():
     f = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
     i = lambda n: torch.zeros(n, dtype=torch.int32)
