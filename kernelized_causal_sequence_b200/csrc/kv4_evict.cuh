@@ -8,7 +8,10 @@
 // each, which the CTAs of a cluster add up through distributed shared memory.
 // Softmax weights crowd into a few bins, so a warp first joins its equal
 // digits (match_any) and adds once for each.  (Bit by bit with a count for each
-// the same search took 33 block-wide sums, 21 us for 300 positions.)  Positions
+// the same search took 33 block-wide sums, 21 us for 300 positions.)  16 x 8 rows
+// of up to 8192 positions, d 128, cut to 2048: 28 us, a third of the DRAM rate,
+// bound by the search's chain of block-wide steps; 300 positions: 12 us (76 and
+// 34 as separate kernels for selecting and copying).  Positions
 // are then ranked by ballots and two prefix sums (those equal to the least key
 // stay from the lowest on), listed, and their rows copied, eight threads each.
 #pragma once

@@ -10,7 +10,8 @@
 //   o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = scale log2(e) q.k_j.
 // 256 threads as 16 x 16; a thread owns BM/16 rows x 4 keys of the scores and
 // BM/16 rows x D/16 channels of the output.  The next tile's keys and values
-// travel to registers while a tile is computed.
+// travel to registers while a tile is computed.  Bound by latency for short prompts
+// (four of up to 64 tokens, 8 heads, d 64: 8.3 us with BM 16, 12.4 with 64).
 #pragma once
 #include "common.cuh"
 #include "packed.cuh"

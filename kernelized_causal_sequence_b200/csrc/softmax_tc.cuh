@@ -21,13 +21,21 @@
 // blocks almost never.
 //
 // The two slots (or two CTAs of one) alternate on the tensor core: while one
-// slot's exponentials run, the products of the other do.  At d 128 the products
-// are the bound (leaving all exponentials out changes a long prompt's time by
-// 1%); they run at what the tensor core gets from shared memory, whose reads
-// for Q K^T (8 KB per 128 x 128 x 16 product) and P V and whose fills together
-// take as long as the products.  At d 64 the products are half as long and the
-// softmax is the bound (226 us with, 170 us without it when this was tried: 8192
-// tokens, 16 heads; 200 us now).
+// slot's exponentials run, the products of the other do.
+//
+// What bounds it.  d 128, 16384 tokens, 16 heads on 2: 910 us, 1.2 PFLOP/s, the
+// tensor pipe active 51% of the time.  Without the exponentials it takes 894 us,
+// without maximum and sum too 891, with half the products 784, with an eighth
+// of the products and none of that arithmetic 513: neither the products nor the
+// arithmetic alone, but the chain S -> TMEM load -> P -> TMEM store -> product,
+// with a barrier at each arrow, of which two per SM run by turns and three do
+// not fit TMEM.  Half blocks (S of 64 keys in two buffers, so that a slot's next
+// scores are there while it works) shorten the chain and were slower, 1156 us
+// for 910 and 380 for 317 on eight packed prompts: a product with N = 64 reads
+// Q as often as one with 128.  d 64, 32 prompts up to 700 tokens: 45 us, of
+// which copies and the first products before any softmax are a good part; for
+// long prompts the softmax is the bound (226 us with, 170 us without it when this
+// was tried: 8192 tokens, 16 heads; 200 us now).
 // Computing part of the exponentials on the FMA units gained nothing: a warp's
 // issue, not the special-function unit, sets the softmax's pace.
 //
