@@ -5,8 +5,8 @@
 // codes are one store of D / 16 bytes, and a group's minimum, maximum and
 // largest magnitude take three shuffles.  Each input is read once and each
 // cache byte written once.  Appending is bound by instruction issue (9.2k tokens
-// x 8 heads, d 128, bf16: 27 us, 567 instructions per warp and 4 rows, IPC 3.1;
-// the bytes alone would be 14 us): exact rounding of scale, offset and code costs
+// x 8 heads, d 128, bf16: 25 us, over 450 instructions per warp and 4 rows at an
+// IPC of 3; the bytes alone would be 14 us): exact rounding of scale, offset and code costs
 // them, in fp32 with fp64 only where a quotient is near a border (58 us in fp64
 // throughout).  Several rows per warp one after the other were slower, as their
 // loads then wait for each other.  Reading back is bound by memory (the same rows
@@ -53,6 +53,31 @@ __device__ __forceinline__ long kv4_row(const Kv4AppendParams &p, int t, int hea
     return ((long)s * p.c.Hkv + head) * p.c.cap + pos;
 }
 
+// The same for the four tokens of a warp (lane l: token t of its eight lanes), of at most 32 sequences: lane s holds
+// sequence s's tokens and start, and a ballot over them finds a token's sequence.  Whole warp; t0 the first token.
+// (12 sequences, 9.2k tokens x 8 heads, append and read: 44.5 us, by bisection in each lane, a chain of loads, 46.2.)
+__device__ __forceinline__ long kv4_row_of_few(const Kv4AppendParams &p, int t0, int head) {
+    const int lane = threadIdx.x & 31, B = p.c.B;
+    int begin = 0, end = 0, start = 0;
+    if (lane < B) {
+        begin = seq_start(p.cu, lane, p.N);
+        end = seq_start(p.cu, lane + 1, p.N);
+        start = p.start[lane];
+    }
+    uint32_t at = 0u;   // sequences that begin at or before the token
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t x = __ballot_sync(0xffffffffu, lane < B && begin <= t0 + j);
+        if (lane >> 3 == j) at = x;
+    }
+    const int s = at ? 31 - __clz(at) : 0, t = t0 + (lane >> 3);
+    const int i = t - __shfl_sync(0xffffffffu, begin, s);
+    end = __shfl_sync(0xffffffffu, end, s);
+    const long pos = (long)__shfl_sync(0xffffffffu, start, s) + i;
+    if (i < 0 || t >= end || pos < 0 || pos >= p.c.cap) return -1;
+    return ((long)s * p.c.Hkv + head) * p.c.cap + pos;
+}
+
 template <int D> struct Kv4Chunk;   // a chunk: one 16-bit field per group
 template <> struct Kv4Chunk<32> { using type = uint16_t; };
 template <> struct Kv4Chunk<64> { using type = uint32_t; };
@@ -78,7 +103,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(Kv4AppendPar
         if (t < p.N) f = load4<InT>(x + (long)t * ts + g * kKv4Group + r * 4);
         v[g][0] = f.x; v[g][1] = f.y; v[g][2] = f.z; v[g][3] = f.w;
     }
-    const long row = t < p.N ? kv4_row(p, t, head) : -1;
+    long row;
+    if (p.cu && p.c.B <= 32) row = kv4_row_of_few(p, t & ~3, head);
+    else row = t < p.N ? kv4_row(p, t, head) : -1;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         lo[g] = min_nan(min_nan(v[g][0], v[g][1]), min_nan(v[g][2], v[g][3]));

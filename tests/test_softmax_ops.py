@@ -428,6 +428,34 @@ def test_append_nonfinite_strided_and_dropped(la):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n_seq", [1, 2, 31, 32, 33, 70])
+def test_append_finds_rows(la, n_seq):
+    """Each token reaches its own sequence and position, with empty sequences
+    among them and behind; what starts outside the cache, and tokens behind the
+    last sequence, are dropped; other rows stay."""
+    Hkv, cap, d = 2, 9, 32
+    lens = [(3 * s + 5) % 7 * (s % 5 != 1) for s in range(n_seq)]
+    first = [(5 * s) % 11 - 2 for s in range(n_seq)]
+    n = sum(lens)
+    x = torch.randn(2 * Hkv, n + 6, d, generator=torch.Generator().manual_seed(n_seq))
+    cache = new_cache(la, n_seq, Hkv, cap, d)
+    want = [t.cpu().clone() for t in cache]
+    la.la_kv4_append(x[:Hkv].to(DEV), x[Hkv:].to(DEV), cache, torch.tensor(first, dtype=torch.int32, device=DEV),
+                     cu_seqlens=cu_of(lens))
+    rows = [rows_ref(x[:Hkv]), rows_ref(x[Hkv:])]
+    t = 0
+    for s in range(n_seq):
+        for i in range(lens[s]):
+            if 0 <= first[s] + i < cap:
+                for j, (b, w) in enumerate(rows):
+                    want[2 * j][s, :, first[s] + i] = b[:, t]
+                    want[2 * j + 1][s, :, first[s] + i] = w[:, t]
+            t += 1
+    for got, ref in zip(cache, want):
+        assert torch.equal(got.cpu(), ref)
+
+
+@pytest.mark.gpu
 def test_read_tokens_of_no_sequence(la):
     c = new_cache(la, 2, 1, 4, 32)
     k, v = la.la_kv4_read(c, torch.zeros(2, dtype=torch.int32, device=DEV), 6, cu_seqlens=cu_of([1, 2]))
