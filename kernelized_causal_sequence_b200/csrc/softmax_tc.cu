@@ -62,16 +62,16 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned
 }
 
 // Which slots (us, 16 query heads; one tile / two slots; S sequences of L tokens):
-//   d 128, 4 key heads   64 x 200: 63 / 67, 16 x 1000: 112 / 113, 8 x 2048: 166 / 161, 1 x 8192: 261 / 250
-//   d 128, 16 key heads  64 x 200: 64 / 73, 16 x 1000: 116 / 122, 8 x 2048: 173 / 171, 1 x 8192: 271 / 259
-//   d 128, 1 x 2048      41 / 45 (too few tiles of two slots)
+//   d 128, 4 key heads   64 x 200: 62 / 59, 32 x 512: 82 / 77, 16 x 1000: 111 / 103, 8 x 2048: 164 / 150, 1 x 8192: 258 / 242
+//   d 128, 16 key heads  64 x 200: 66 / 67, 32 x 512: 85 / 83, 16 x 1000: 114 / 107, 8 x 2048: 170 / 156, 1 x 8192: 269 / 268
+//   d 128, 1 x 4096      78 / 75 and 78 / 77; 1 x 2048: 40 / 42 and 40 / 43 (too few tiles of two slots)
 //   d 64                 one tile up to 8192 tokens (1 x 8192: 200 / 209): the softmax bounds it there
 // Two slots read a key and value tile once for both, which counts where the
 // products' operands bound it; one tile leaves less empty and more to overlap.
 template <typename InT, typename OutT, int D>
 la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {
     if constexpr (D == 128) {
-        if ((long)sp.N > 1024L * sp.n_seq && (long)seq_tiles(sp.N, sp.n_seq, 256) * sp.H >= 2L * kNumSMs) {
+        if ((long)sp.N > 256L * sp.n_seq && 2L * seq_tiles(sp.N, sp.n_seq, 256) * sp.H >= 3L * kNumSMs) {
             if (sp.group % 2 == 0) return run<InT, OutT, D, stc::kTwoHeads>(sp, dt, d, status, wait_ns, st);
             return run<InT, OutT, D, stc::kTwoTiles>(sp, dt, d, status, wait_ns, st);
         }

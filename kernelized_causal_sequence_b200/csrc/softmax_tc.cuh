@@ -23,19 +23,20 @@
 // The two slots (or two CTAs of one) alternate on the tensor core: while one
 // slot's exponentials run, the products of the other do.
 //
-// What bounds it.  d 128, 16384 tokens, 16 heads on 2: 910 us, 1.2 PFLOP/s, the
-// tensor pipe active 51% of the time.  Without the exponentials it takes 894 us,
-// without maximum and sum too 891, with half the products 784, with an eighth
-// of the products and none of that arithmetic 513: neither the products nor the
-// arithmetic alone, but the chain S -> TMEM load -> P -> TMEM store -> product,
-// with a barrier at each arrow, of which two per SM run by turns and three do
-// not fit TMEM.  Half blocks (S of 64 keys in two buffers, so that a slot's next
-// scores are there while it works) shorten the chain and were slower, 1156 us
-// for 910 and 380 for 317 on eight packed prompts: a product with N = 64 reads
-// Q as often as one with 128.  d 64, 32 prompts up to 700 tokens: 45 us, of
-// which copies and the first products before any softmax are a good part; for
-// long prompts the softmax is the bound (226 us with, 170 us without it when this
-// was tried: 8192 tokens, 16 heads; 200 us now).
+// What bounds it.  d 128, 16384 tokens, 16 heads on 2: 896 us, 1.2 PFLOP/s.  Measured
+// when it took 910: the tensor pipe active 51% of the time; without the
+// exponentials 894 us, without maximum and sum too 891, with half the products
+// 784, with an eighth of the products and none of that arithmetic 513.  So it is
+// neither the products nor the arithmetic alone, but the chain S -> TMEM load ->
+// P -> TMEM store -> product, with a barrier at each arrow, of which two per SM
+// run by turns and three do not fit TMEM.  Half blocks (S of 64 keys in two
+// buffers, so that a slot's next scores are there while it works) shorten the
+// chain and were slower, 1156 us for 910: a product with N = 64 reads Q as often
+// as one with 128.  P handed over in halves, so that its first product runs under
+// the second half's exponentials, was slower too (912 for 896).  d 64, 32 prompts
+// up to 700 tokens: 45 us, of which copies and the first products before any
+// softmax are a good part; for long prompts the softmax is the bound (226 us with,
+// 170 us without it when this was tried: 8192 tokens, 16 heads; 200 us now).
 // Computing part of the exponentials on the FMA units gained nothing: a warp's
 // issue, not the special-function unit, sets the softmax's pace.
 //
@@ -77,7 +78,7 @@ constexpr float kLazyLog2 = 8.f;   // how far (log2) the maximum may outgrow the
 
 template <int D, int MODE> struct Cfg {
     static constexpr int SLOTS = MODE == kOneTile ? 1 : 2;
-    static constexpr int THREADS = SLOTS == 1 ? 256 : 352;
+    static constexpr int THREADS = SLOTS == 1 ? 256 : 384;
     static constexpr int TMA_WARP = 4 * SLOTS, MMA_WARP = TMA_WARP + 1, SCRUB_WARP = TMA_WARP + 2;
     static constexpr int KB = D / 64;                  // 128-byte boxes per row
     static constexpr int BOXB = kBlock * 128;
@@ -295,11 +296,13 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         return w;
     };
 
-    // One slot: the softmax warps need more registers than the 128 that two
-    // CTAs of 256 threads leave each; 128 x 200 + 128 x 56 is what there is.
-    // (Two slots: 352 threads have 168, which is enough.)
+    // The softmax warps get registers of the others: of the 256 x 128 of a CTA of
+    // one slot 128 x 200 + 128 x 56, of the 384 x 168 of two slots 256 x 216 +
+    // 128 x 56 (never more than the CTA was launched with: an increase would wait
+    // for good).  With 168 for all, two slots took 917 us for 896 (16384 tokens,
+    // 16 heads on 2) and 317 for 304 (eight packed prompts).
     if (warp >= G::TMA_WARP) {
-    if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == G::TMA_WARP) {
         // ================= the list of tiles, and the copies
         if (lane == 0) {
@@ -490,6 +493,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
     } else {
         if constexpr (G::SLOTS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // softmax of slot s: thread = row
         const int s = warp >> 2, q = warp & 3;
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
