@@ -46,6 +46,11 @@
 // the row's end; a row cut between CTAs is joined by kv4_finish_kernel.
 // Short caches are dealt out by whole rows instead and need no second kernel
 // (16 x 16 rows, lengths to 2048 at d 64: 18.0 / 16.5 us).
+//
+// What bounds it.  64 sequences of up to 8192 positions, 16 heads on 4, d 128,
+// bf16: 55 us for 168 MB (26 us at the copy rate); the integer pipe is 54% busy
+// and the SM issues 2.5 of 4 instructions a cycle, about 1000 per tile of 32
+// positions, of which the unpacking of the codes alone is a third.
 #pragma once
 #include <type_traits>
 

@@ -166,6 +166,9 @@ PREFILL = [
     (torch.bfloat16, None, 128, 3, 3, [1, 130, 77, 0, 256, 383, 300], 65),
     (torch.float16, torch.float32, 128, 1, 1, [255, 129, 128, 1], 0),
     (torch.bfloat16, torch.float32, 128, 3, 1, [700, 384, 900], 3),
+    # two tiles and two heads over sequences of every length, empty ones among them
+    (torch.bfloat16, None, 128, 9, 3, [0, 1, 255, 256, 257, 0, 384, 513, 900, 1300, 64, 1100], 11),
+    (torch.float16, torch.float32, 128, 12, 2, [65, 0, 0, 1200, 128, 129, 640, 1, 511, 383, 0, 1700], 0),
 ]
 
 
