@@ -47,6 +47,9 @@ struct EvictShared {
     uint32_t slots[2][kEvictMaxCluster];   // the CTAs' counts, by turns
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // The sum of x (a CTA's own number, the same in all threads) over the CTAs of lower rank.  `turn` alternates the
 // slots: a CTA can be one exchange ahead of another, not two.
 __device__ __forceinline__ uint32_t sum_before(EvictShared &sh, uint32_t x, int cs, int rank, int &turn) {
@@ -92,6 +95,9 @@ template <int D, int THREADS> __global__ void __launch_bounds__(THREADS) kv4_evi
     constexpr int G = D / kKv4Group, KPT = kEvictKeys, SPAN = KPT * THREADS, NW = THREADS / 32;
     using Chunk = typename Kv4Chunk<D>::type;
     __shared__ EvictShared sh;
+    // A CTA's shared memory may be reached into only once that CTA runs: every CTA of the cluster says so here, and
+    // waits for the others below, before its first access to theirs.
+    if (cs > 1) cluster_arrive();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x % cs, bh_i = blockIdx.x / cs;
@@ -116,6 +122,7 @@ template <int D, int THREADS> __global__ void __launch_bounds__(THREADS) kv4_evi
         }
     };
     load(0);
+    if (cs > 1) cluster_wait();
     // the least key that stays, and how many equal to it do
     uint32_t least = 0xffffffffu, equal = 0;
     if (need > 0) {

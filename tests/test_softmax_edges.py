@@ -1,0 +1,48 @@
+"""The softmax operators where single calls went, or could go, wrong: masks and
+weights at the ends of the types' ranges, clusters with nothing to choose,
+long lists of tiles, empty extents, arguments that alias.
+
+References and bounds are those of test_softmax_ops, whose notation is used:
+u = half a step of a type, A = sum_j p_j |v_j|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_softmax_ops import DEV, ref_evict
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hkv,cap,lens,keep,recent", [
+    # clusters (caches beyond 8192 positions, few rows) whose rows have nothing to choose: within the budget, empty,
+    # or with the newest positions alone
+    (64, 1, 20000, [20000, 50, 0], 100, 100),
+    (32, 2, 20000, [50, 20000, 0], 1000, 0),
+    (128, 1, 9000, [9000, 9000], 9000, 0),
+    (32, 1, 70000, [70000, 3], 500, 500),
+    (32, 1, 70000, [400, 0, 500, 70000], 500, 250),
+])
+def test_evict_clusters_with_nothing_to_choose(la, d, Hkv, cap, lens, keep, recent):
+    B = len(lens)
+    rng = np.random.default_rng(cap + keep)
+    c = la.KV4Cache.alloc(B, Hkv, cap, d, DEV)
+    for x in c:
+        x.view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 256, size=tuple(x.view(torch.uint8).shape), dtype=np.uint8)))
+    w = rng.random((B, Hkv, cap)).astype(np.float32)
+    wd, ld = torch.from_numpy(w).to(DEV), i32(*lens)
+    for _ in range(20):
+        out, kept, ow, ol = la.la_kv4_evict(c, wd, ld, keep, recent=recent)
+        assert ol.tolist() == [min(n, keep) for n in lens]
+        for b in range(B):
+            for h in range(Hkv):
+                want = ref_evict(w[b, h].tolist(), lens[b], keep, recent)
+                m = len(want)
+                assert kept[b, h].tolist() == want + [-1] * (keep - m)
+                assert ow[b, h, :m].tolist() == w[b, h, want].tolist() and (ow[b, h, m:] == 0).all()
+                for x, y in zip(c, out):
+                    assert torch.equal(y[b, h, :m], x[b, h, want])
