@@ -376,8 +376,11 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     } else if (warp == G::MMA_WARP) {
         // The whole warp goes through the waits and the index arithmetic, so that
         // the descriptors are uniform values, ready before the last wait; one
-        // thread issues the products and the commits.  (No vote on the waits: a lane
-        // that gives up goes to the end, and nothing here needs the others with it.)
+        // thread issues the products and the commits.  Before its commits, which let
+        // others go on, a vote makes sure that every lane is through its waits: a lane
+        // left behind by two phases would wait for one that has passed.  The vote runs
+        // under the products (16384 tokens, 16 heads on 2: 917 us; ahead of them 930, the
+        // waits in one thread alone 957).
         constexpr bool BF = std::is_same<InT, bf16>::value;
         constexpr uint32_t ID_S = BF ? idesc_bf16(128, 128, false, false) : idesc_f16(128, 128, false, false);
         constexpr uint32_t ID_O = BF ? idesc_bf16(128, D, false, true) : idesc_f16(128, D, false, true);
@@ -393,8 +396,9 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             return f;
         };
         for (int k = 0; ok; ++k) {
-            const Work w = next_work(k, wait_bar(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10));
+            const Work w = next_work(k, wait_warp(&bar[G::B_WORK + (k & 3)], (k >> 2) & 1, ab, 10));
             if (w.head < 0) break;
+            __syncwarp();   // every lane has read the entry
             if (leader) mbar_arrive(&bar[G::B_WORK_EMPTY + (k & 3)]);
             const int n0 = blocks0(w), n1 = blocks1(w, n0), nb = max(n0, n1);
             // step j: per slot P V_j, then S of block j + 1
@@ -413,25 +417,23 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                 for (int s = 0; s < G::SLOTS; ++s) {
                     const int n = s ? n1 : n0;
-                    if (n == 0 || j >= n || !ok) continue;
+                    if (n == 0 || j >= n) continue;   // (one slot at least goes on, to the vote on the waits above)
                     const uint32_t to = tmem + G::T_O + 128 * s, ts = tmem + G::T_S + 128 * s;
                     if (j >= 0) {
                         // (a new tile's first product overwrites O: its last one has been read out)
-                        if (j == 0 && ((had >> s) & 1)) ok = wait_bar(&bar[G::B_O_EMPTY + s], ((tile_phase >> s) & 1) ^ 1, ab, 13);
+                        if (j == 0 && ((had >> s) & 1))
+                            ok = ok && wait_bar(&bar[G::B_O_EMPTY + s], ((tile_phase >> s) & 1) ^ 1, ab, 13);
                         ok = ok && wait_bar(&bar[G::B_P + s], (block_phase >> s) & 1, ab, 5);
-                        if (!ok) continue;
                         block_phase ^= 1u << s;
                     } else {
-                        ok = wait_bar(&bar[G::B_Q + s], (tile_phase >> s) & 1, ab, 3);
-                        if (!ok) continue;
+                        ok = ok && wait_bar(&bar[G::B_Q + s], (tile_phase >> s) & 1, ab, 3);
                     }
                     tc_fence_after();
-                    if (leader) {
+                    if (leader && ok) {
                         if (j >= 0) {
 #pragma unroll
                             for (int kk = 0; kk < kBlock / 16; ++kk)
                                 mma_ts(to, ts + kk * 8, bv + (uint64_t)((kk * 2048) >> 4), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
-                            if (j == n - 1) mma_commit(&bar[G::B_O + s]);
                         }
                         if (j + 1 < n) {
                             const uint64_t a = sdesc_sw128(sb + G::OFF_Q + s * G::TILE, 16, 1024);
@@ -440,6 +442,13 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                 const uint32_t off = ((kk >> 2) * G::BOXB + (kk & 3) * 32) >> 4;
                                 mma_ss(ts, a + off, bk + off, ID_S, kk > 0);
                             }
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (leader) {
+                        if (j == n - 1) mma_commit(&bar[G::B_O + s]);
+                        if (j + 1 < n) {
                             mma_commit(&bar[G::B_S + s]);
                             if (j + 2 == n) mma_commit(&bar[G::B_Q_EMPTY + s]);
                         }

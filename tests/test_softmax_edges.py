@@ -9,11 +9,33 @@ import numpy as np
 import pytest
 import torch
 
-from test_softmax_ops import DEV, ref_evict
+from test_softmax_ops import DEV, check_prefill, cu_of, prefill_inputs, ref_evict
 
 
 def i32(*x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ prompt attention
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,H,Hkv,lo,hi,S", [(torch.float16, 64, 8, 8, 1, 40, 1500), (torch.bfloat16, 128, 16, 4, 1, 300, 400),
+                                                   (torch.bfloat16, 128, 8, 4, 257, 700, 150), (torch.float16, 128, 9, 9, 257, 700, 100)])
+def test_prefill_long_lists(la, dtype, d, H, Hkv, lo, hi, S):
+    """Tens of tiles a CTA, of every small number of blocks (one tile, two heads, two tiles a CTA): no wait gives up,
+    every run gives the same bits, and the first and last sequences' rows are right."""
+    lens = np.random.default_rng(S).integers(lo, hi + 1, size=S).tolist()
+    N = sum(lens)
+    q, k, v = prefill_inputs(dtype, d, H, Hkv, N, seed=S)
+    ws = torch.empty(la.la_softmax_prefill_workspace_size(H, Hkv, N, d, S), dtype=torch.uint8, device=DEV)
+    dev = [x.to(DEV) for x in (q, k, v)]
+    runs = []
+    for _ in range(5):
+        runs.append(la.la_softmax_prefill(*dev, cu_of(lens), workspace=ws))
+        assert la.la_workspace_status(ws) == (la.LA_OK, 0)
+        assert torch.equal(runs[-1], runs[0])
+    for part, at in ((lens[:20], 0), (lens[-20:], N - sum(lens[-20:]))):
+        r = slice(at, at + sum(part))
+        check_prefill(runs[0][:, r], q[:, r], k[:, r], v[:, r], part, d ** -0.5, True)
 
 
 # ------------------------------------------------------------------ eviction
