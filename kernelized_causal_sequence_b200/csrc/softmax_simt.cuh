@@ -152,12 +152,13 @@ __global__ void __launch_bounds__(kSsThreads) softmax_simt_kernel(SoftmaxParams 
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             const float mn = fmaxf(m[i], mx);
-            const float f = exp2f(m[i] - mn);
+            const float ref = mn == -INFINITY ? 0.f : mn;   // -inf: nothing yet but scores of -inf, whose weights are 0
+            const float f = exp2f(m[i] - ref);
             m[i] = mn;
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = exp2f(s[i][j] - mn);
+                s[i][j] = exp2f(s[i][j] - ref);
                 sum += s[i][j];
                 ps[(tx * 4 + j) * QP + ty * RW + i] = s[i][j];
             }

@@ -5,11 +5,13 @@ long lists of tiles, empty extents, arguments that alias.
 References and bounds are those of test_softmax_ops, whose notation is used:
 u = half a step of a type, A = sum_j p_j |v_j|.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from test_softmax_ops import DEV, check_prefill, cu_of, prefill_inputs, ref_evict
+from test_softmax_ops import DEV, check_prefill, cu_of, prefill_inputs, ref_evict, tensor_cores
 
 
 def i32(*x):
@@ -36,6 +38,29 @@ def test_prefill_long_lists(la, dtype, d, H, Hkv, lo, hi, S):
     for part, at in ((lens[:20], 0), (lens[-20:], N - sum(lens[-20:]))):
         r = slice(at, at + sum(part))
         check_prefill(runs[0][:, r], q[:, r], k[:, r], v[:, r], part, d ** -0.5, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,H", [(torch.float32, 32, 2), (torch.float32, 64, 80), (torch.float32, 128, 2), (torch.bfloat16, 64, 2),
+                                       (torch.bfloat16, 128, 2), (torch.float16, 128, 2)])
+@pytest.mark.parametrize("first", [1, 64, 130])
+def test_prefill_scores_of_minus_infinity(la, dtype, d, H, first):
+    """Keys with an infinite channel score -inf.  Rows that see others too are the softmax of those, however many
+    keys of -inf come before, between or behind; rows that see no other are 0 / 0."""
+    n = first + 300
+    q, k, v = prefill_inputs(dtype, d, H, 2, n, seed=first + d)
+    q[..., 0] = 1
+    kk = k.clone()
+    kk[:, :first, 0] = -math.inf
+    out = la.la_softmax_prefill(q.to(DEV), kk.to(DEV), v.to(DEV), cu_of([n]))
+    assert torch.isnan(out[:, :first]).all()
+    check_prefill(out[:1, first:], q[:1, first:], k[:1, first:], v[:1, first:], [n - first], d ** -0.5, tensor_cores(dtype, d))
+    # among the others: as if they were not there
+    kk, gap = k.clone(), slice(40, 40 + first)
+    kk[:, gap, 0] = -math.inf
+    out = la.la_softmax_prefill(q.to(DEV), kk.to(DEV), v.to(DEV), cu_of([n]))
+    rest = lambda x: torch.cat([x[:, :40], x[:, 40 + first:]], 1)
+    check_prefill(rest(out)[:1], rest(q)[:1], rest(k)[:1], rest(v)[:1], [n - first], d ** -0.5, tensor_cores(dtype, d))
 
 
 # ------------------------------------------------------------------ eviction
