@@ -348,8 +348,9 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  *   out    must not overlap the inputs
  * Keys and values behind a query, or of another sequence, do not reach it,
  * not even as NaN or infinity.  Sums and the running maximum are fp32; with
- * 16-bit inputs (the tensor-core kernel) the unnormalised weights, which lie
- * in [0, 256], are rounded once to the input type for the product with v.
+ * 16-bit inputs (the tensor-core kernel) the unnormalised weights are rounded
+ * once to the input type for the product with v: relative to themselves, but
+ * in fp16 those below 2^-25 of a row's greatest to a multiple of 2^-35 of it.
  * The workspace (la_softmax_prefill_workspace_size bytes, 256-byte aligned)
  * starts with the status word that la_workspace_status reads.  Calls that may
  * overlap on the GPU need workspaces of their own (here and below).

@@ -9,16 +9,17 @@
 //
 //   S = Q K_j^T                     tcgen05, fp32 in TMEM
 //   m' = max(m, rowmax S)           the reference of the exponents moves only
-//                                   where m' - m > 8 / c, see below
-//   P = 2^(c S - c m), l += rowsum  P rounded once to the input type, in TMEM
+//                                   where c (m' - m) > kLazy, see below
+//   P = 2^(c S - c m + kUp)         rounded once to the input type, in TMEM
+//   l += rowsum P                   fp32, unrounded
 //   O += P V_j                      tcgen05, fp32 in TMEM
 //   out = O / l
 //
 // Moving the reference multiplies O and l by 2^(c (m - m')).  O lives in TMEM,
 // so this is a read and a write of the whole accumulator; a reference that is
-// up to 2^8 too small costs nothing (P <= 256, and neither type's relative
-// rounding depends on it), so it is moved only beyond that: after the first
-// blocks almost never.
+// up to 2^kLazy too small costs nothing (bf16 has fp32's exponents; fp16 has room
+// for it above kUp), so it is moved only beyond that: after the first blocks almost
+// never.
 //
 // The two slots (or two CTAs of one) alternate on the tensor core: while one
 // slot's exponentials run, the products of the other do.
@@ -74,7 +75,13 @@ constexpr int kBlock = 128;   // keys of a block, rows of a slot
 // What the slots of a CTA are: one tile of queries (two CTAs per SM), two
 // consecutive tiles of one head, or the same tile of two heads.
 enum Slots { kOneTile = 0, kTwoTiles = 1, kTwoHeads = 2 };
-constexpr float kLazyLog2 = 8.f;   // how far (log2) the maximum may outgrow the reference
+// kLazy: how far (log2) the maximum may outgrow the reference.  kUp: power of two on P, l and O (O / l drops it).
+// bf16 has fp32's range.  fp16's is used up to 2^15: weights down to 2^-25 of the row's greatest are normal numbers,
+// rounded relative to themselves, smaller ones to a multiple of 2^-35 of it.  (With 8 and 0 that ended at 2^-14, and
+// beside a key with 2^24 of their weight the others were rounded to that step or to nothing.  In fp16, 16384 tokens,
+// 16 heads on 2: 920 us with 4 and 11, 923 with 8 and 7, 930 with 2 and 13.)
+template <typename InT> constexpr float kLazy = std::is_same<InT, f16>::value ? 4.f : 8.f;
+template <typename InT> constexpr float kUp = std::is_same<InT, f16>::value ? 11.f : 0.f;
 
 template <int D, int MODE> struct Cfg {
     static constexpr int SLOTS = MODE == kOneTile ? 1 : 2;
@@ -540,7 +547,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (j == 0) {
                     m = mn;
                 } else {
-                    const bool move = (mn - m) * c > kLazyLog2;   // (m = -inf: infinite; mn = -inf: NaN, false)
+                    const bool move = (mn - m) * c > kLazy<InT>;   // (m = -inf: infinite; mn = -inf: NaN, false)
                     if (__any_sync(0xffffffffu, move)) {
                         const float f = move ? ex2_approx((m - mn) * c) : 1.f;
 #pragma unroll 1
@@ -556,7 +563,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         m = move ? mn : m;
                     }
                 }
-                const float neg = m == -INFINITY ? 0.f : -m * c;
+                const float neg = m == -INFINITY ? 0.f : fmaf(-m, c, kUp<InT>);
                 const uint64_t c2 = pack2(c, c), n2 = pack2(neg, neg);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll

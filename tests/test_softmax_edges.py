@@ -63,6 +63,25 @@ def test_prefill_scores_of_minus_infinity(la, dtype, d, H, first):
     check_prefill(rest(out)[:1], rest(q)[:1], rest(k)[:1], rest(v)[:1], [n - first], d ** -0.5, tensor_cores(dtype, d))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,H,Hkv", [(torch.float16, 64, 1, 1), (torch.float16, 128, 30, 2), (torch.float16, 128, 37, 37),
+                                           (torch.bfloat16, 64, 1, 1), (torch.float32, 64, 1, 1)])
+@pytest.mark.parametrize("bits", [4, 12, 20, 24])
+@pytest.mark.parametrize("at", [0, 400])
+def test_prefill_one_key_takes_the_weight(la, dtype, d, H, Hkv, bits, at):
+    """A key of value 0 with 2^bits of every other key's weight: what is left of the output is made of the small
+    weights alone, each of which keeps its relative precision (down to 2^-25 of the greatest)."""
+    n = 3000 if H > 1 else 1500
+    g = torch.Generator().manual_seed(bits + d)
+    q, k = torch.zeros(H, n, d, dtype=dtype), torch.zeros(Hkv, n, d, dtype=dtype)
+    q[..., 0] = 1
+    k[..., 0] = (-(bits + torch.rand(Hkv, n, generator=g)) * math.log(2)).to(dtype)
+    v = torch.randn(Hkv, n, d, generator=g).to(dtype)
+    k[:, at], v[:, at] = 0, 0
+    out = la.la_softmax_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([n]), scale=1.0, out_dtype=torch.float32)
+    check_prefill(out[:1], q[:1], k[:1], v[:1], [n], 1.0, tensor_cores(dtype, d))
+
+
 # ------------------------------------------------------------------ eviction
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,Hkv,cap,lens,keep,recent", [
