@@ -427,7 +427,9 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
  * The products run on the tensor cores in fp16 terms, scaled by powers of two:
  * 4-bit codes and 16-bit queries are exact there; the weights times the
  * values' scales are rounded once to fp16's 11 bits (16-bit queries) or carried
- * as two terms, like fp32 queries.  Sums are fp32.
+ * as two terms, like fp32 queries: relative to themselves, down to 2^-26 of the
+ * greatest weight times the largest scale, and below that to a multiple of
+ * 2^-36 of it (the second of two terms too).  Sums are fp32.
  */
 la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_cache *cache, const int32_t *lens,
                         float scale, const float *weights_in, float *weights_out, void *out,

@@ -21,9 +21,12 @@
 // of two per head that brings the largest to [2^10, 2^11): 16-bit ones are then
 // one fp16 term (bf16: exact down to 2^-35 of the largest), fp32 ones two
 // (2^-23 of the largest).  p s is scaled by a power of two, so that fp16 holds
-// it whatever the values' magnitude (at most 2^15, and to 2^-32 of the largest
-// scale), and rounded once (16-bit queries; 2^-11 of itself) or carried as two
-// terms (fp32); the second sum uses the same rounded number.  With fp32 queries
+// it whatever the values' magnitude (at most 2^15), and rounded once (16-bit
+// queries; 2^-11 of itself) or carried as two terms (fp32); the second sum uses the
+// same rounded number.  Products down to 2^-26 of the largest scale (p = 1 at the
+// reference) are normal numbers, smaller ones a multiple of 2^-36 of it.  (Held
+// 2^6 lower, with a reference moved at 2^8, a position of value 0 with 2^24 of the
+// others' weights left those 2^-7 of themselves off.)  With fp32 queries
 // tensor-core sums run over one tile of 32 positions only and are joined in
 // fp32: the tensor core cuts its sums off instead of rounding, 2^-24 of them
 // each time, which over a long cache would be seen at fp32's precision.
@@ -37,7 +40,7 @@
 // product's k index: the softmax and p s are formed in that layout.  Rows are
 // assigned to positions so that the value loads of a phase fall into both
 // halves of the banks (row_pos).  Each warp keeps its own reference maximum per
-// head, moved only when exceeded by 2^8 (as in the prompt kernel).
+// head, moved only when exceeded by 2^kDecLazy (as in the prompt kernel).
 //
 // Work is dealt out by the lengths, which only the device knows: the tiles of
 // all rows (a sequence's key/value head, and block of query heads) lie on one
@@ -77,7 +80,7 @@ struct Kv4DecodeParams {
 };
 
 constexpr int kDecWarps = 4, kDecTile = 32, kDecStages = 2;
-constexpr float kDecLazy = 8.f;
+constexpr float kDecLazy = 2.f;     // (8 was no faster: 64 rows x 4, lengths to 8192, 64.3 us for 64.5)
 constexpr int kDecCtas = 3;         // CTAs per SM with up to 8 query heads (more: 2)
 constexpr int kDecMinTiles = 16;    // places of a CTA at least: three or four tiles a warp, to hide its start
 constexpr int kDecRowCost = 8;      // tiles' worth of time (of four warps) that a row's start and join take
@@ -383,13 +386,13 @@ __device__ __forceinline__ void decode_row(const Kv4DecodeParams &p, uint8_t *de
                 const uint32_t bits = vw[g] << 16;
                 if (bits < 0x7f800000u) big = max(big, bits);   // (a group of NaN is its own: it sets no unit)
             }
-            // The unit grows with the largest scale met (in [2^e, 2^(e + 1)): p s < 2^8 2^(e + 1) = 2^15 unit);
+            // The unit grows with the largest scale met (in [2^e, 2^(e + 1)): p s < 2^kDecLazy 2^(e + 1) = 2^15 unit);
             // one-term queries sum their products in it from tile to tile.
             if (TILE_SUMS || __any_sync(0xffffffffu, big >= unit_end)) {
-                const uint32_t e = max(__reduce_max_sync(0xffffffffu, big) >> 23, 7u);
+                const uint32_t e = max(__reduce_max_sync(0xffffffffu, big) >> 23, 13u);
                 const float old = unit;
-                unit = __uint_as_float((e - 6u) << 23);
-                per_unit = __uint_as_float((260u - e) << 23);
+                unit = __uint_as_float((e - 12u) << 23);
+                per_unit = __uint_as_float((266u - e) << 23);
                 unit_end = (e + 1u) << 23;
                 if (!TILE_SUMS && old > 0.f) {
                     const float f = old / unit;

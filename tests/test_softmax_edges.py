@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_softmax_ops import DEV, check_prefill, cu_of, prefill_inputs, ref_evict, tensor_cores
+from test_softmax_ops import DEV, U, U32, check_prefill, cu_of, fill_cache, pack_ref, prefill_inputs, ref_evict, tensor_cores
 
 
 def i32(*x):
@@ -80,6 +80,46 @@ def test_prefill_one_key_takes_the_weight(la, dtype, d, H, Hkv, bits, at):
     k[:, at], v[:, at] = 0, 0
     out = la.la_softmax_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([n]), scale=1.0, out_dtype=torch.float32)
     check_prefill(out[:1], q[:1], k[:1], v[:1], [n], 1.0, tensor_cores(dtype, d))
+
+
+# ------------------------------------------------------------------ decode
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H", [(torch.float16, 4), (torch.bfloat16, 4), (torch.bfloat16, 12), (torch.float32, 4)])
+@pytest.mark.parametrize("T", [2, 20, 150])
+@pytest.mark.parametrize("bits", [4, 12, 20, 24])
+def test_decode_one_position_takes_the_weight(la, dtype, H, T, bits):
+    """A position of value 0 with 2^bits of every other one's weight: what is left of the output is made of the
+    small weights alone, each of which keeps its relative precision (times its scale, down to 2^-26 of the largest
+    scale).
+
+    Bound.  A score is one product (the queries have one channel): a code's exact number and an offset, both up to 31
+    scales, in at most 8 roundings of fp32.  A weight's exponential and the sums as in ref_decode, over n positions
+    of which each product is at most 31 scales (16 of code, 15 of offset and the constant 8).  The product p scale is
+    rounded to 11 bits, or carried as two terms of 22 bits, at worst to half a step of 2^-36 of the largest scale (fp32
+    queries); that number then multiplies a value over its scale, at most 16."""
+    d = 64
+    g = torch.Generator().manual_seed(bits + T)
+    q = torch.zeros(1, H, d, dtype=dtype)
+    q[..., 0] = 1
+    k = torch.zeros(1, 1, T, d)
+    k[..., 0] = -(bits + 0.4 * torch.rand(1, 1, T, generator=g)) * math.log(2)
+    v = torch.randn(1, 1, T, d, generator=g)
+    k[0, 0, T // 2], v[0, 0, T // 2] = 0, 0
+    cache, kv, vv = fill_cache(la, k, v)
+    out = la.la_kv4_decode(q.to(DEV), cache, i32(T), scale=1.0, out_dtype=torch.float32)
+    s = kv[0, 0, :, 0]
+    p = torch.softmax(s, 0)
+    vs = torch.from_numpy(pack_ref(v)[1])[0, 0].repeat_interleave(32, -1)
+    ref, A = p @ vv[0, 0], p @ vv[0, 0].abs()
+    ks = float(torch.from_numpy(pack_ref(k)[1]).max())
+    rel = 2 * (8 * U32 * 2 * 31 * ks + 4 * U32 * float(s.abs().max())) + 2 * 2.0 ** -20 + 2 * (T + 64) * U32
+    tol = rel * A + (T + 64) * U32 * 31 * (p @ vs) + U32 * ref.abs() + 1e-30
+    if dtype == torch.float32:
+        tol = tol + 2.0 ** -22 * A + T * 2.0 ** -37 * 16 * float(vs.max())
+    else:
+        tol = tol + U[torch.float16] * A
+    err = (out[0].double().cpu() - ref).abs()
+    assert float((err / tol).max()) <= 1.0
 
 
 # ------------------------------------------------------------------ eviction
