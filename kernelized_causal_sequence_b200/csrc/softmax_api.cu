@@ -168,6 +168,7 @@ la_status run_decode_nt(const Kv4DecodeParams &p, cudaStream_t st) {
     const unsigned ob = p.whole ? 0u : (unsigned)p.group;
     // (four positions a thread, at most four blocks per SM)
     const unsigned wb = p.weights_out ? stride_grid(p.c.cap, 4 * kFinThreads, 2L * p.c.Hkv * p.c.B) : 0u;
+    if (ob + wb == 0) return LA_OK;   // (a cache without positions)
     return launch_kernel(kv4_finish_kernel<OutT, D>, dim3(ob + wb, (unsigned)p.c.Hkv, (unsigned)p.c.B),
                          dim3(kFinThreads), 0, st, true, "kv4 finish launch", p, (int)ob);
 }

@@ -122,6 +122,23 @@ def test_decode_one_position_takes_the_weight(la, dtype, H, T, bits):
     assert float((err / tol).max()) <= 1.0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [4, 40])
+@pytest.mark.parametrize("with_weights", [False, True])
+def test_decode_cache_without_positions(la, H, with_weights):
+    """cap 0: zeros, for more query heads than one block takes too, and nothing is written to the weights."""
+    B, d = 2, 64
+    c = la._Kv4CacheC(None, None, None, None, B, 1, 0, d)
+    q = torch.ones(B, H, d, dtype=torch.bfloat16, device=DEV)
+    out, w, lens = torch.full_like(q, 3.0), torch.full((4,), 5.0, device=DEV), i32(0, 7)
+    ws = torch.empty(max(la.la_kv4_decode_workspace_size(B, H, 1, 0, d, with_weights), 256), dtype=torch.uint8, device=DEV)
+    status = la.lib().la_kv4_decode(q.data_ptr(), la.LA_BF16, H, c, lens.data_ptr(), 0.1, None,
+                                    w.data_ptr() if with_weights else None, out.data_ptr(), la.LA_BF16, ws.data_ptr(),
+                                    ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert status == la.LA_OK
+    assert (out == 0).all() and (w == 5.0).all()
+
+
 # ------------------------------------------------------------------ eviction
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,Hkv,cap,lens,keep,recent", [
