@@ -257,9 +257,14 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
     if (s != LA_OK) return s;
     if (!dt_ok(out_dtype) || N < 0 || (!cu_seqlens && N != cache->B)) return LA_ERR_INVALID_ARG;
     if (N > kMaxTokens) return LA_ERR_UNSUPPORTED;
-    if (N == 0 || cache->B == 0 || cache->H_kv == 0) return LA_OK;
-    if (!k_out || !v_out || !start || !al16(k_out) || !al16(v_out) || !al4(start) || !al4(cu_seqlens))
+    if (N == 0 || cache->H_kv == 0) return LA_OK;
+    if (!k_out || !v_out || !al16(k_out) || !al16(v_out) || (cache->B && !start) || !al4(start) || !al4(cu_seqlens))
         return LA_ERR_INVALID_ARG;
+    if (cache->B == 0) {   // tokens of no sequence
+        const size_t n = (size_t)cache->H_kv * N * cache->d * esize(out_dtype);
+        if ((s = cuda_check("kv4 read", cudaMemsetAsync(k_out, 0, n, (cudaStream_t)stream))) != LA_OK) return s;
+        return cuda_check("kv4 read", cudaMemsetAsync(v_out, 0, n, (cudaStream_t)stream));
+    }
     Kv4AppendParams p;
     std::memset(&p, 0, sizeof(p));
     p.cu = cu_seqlens; p.start = start; p.c = dev_cache(cache); p.N = N; p.k_out = k_out; p.v_out = v_out;

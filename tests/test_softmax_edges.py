@@ -82,6 +82,21 @@ def test_prefill_one_key_takes_the_weight(la, dtype, d, H, Hkv, bits, at):
     check_prefill(out[:1], q[:1], k[:1], v[:1], [n], 1.0, tensor_cores(dtype, d))
 
 
+# ------------------------------------------------------------------ reading back
+@pytest.mark.gpu
+@pytest.mark.parametrize("od,dtype", [(torch.float32, "LA_F32"), (torch.bfloat16, "LA_BF16")])
+@pytest.mark.parametrize("B,cap", [(0, 8), (3, 0)])
+def test_read_cache_without_rows(la, od, dtype, B, cap):
+    """Tokens of no sequence, where there is no sequence at all, and positions outside a cache of none: zeros."""
+    Hkv, N, d = 2, 6, 64
+    c = la._Kv4CacheC(None, None, None, None, B, Hkv, cap, d)
+    cu, start = i32(*range(B + 1)), torch.zeros(max(B, 1), dtype=torch.int32, device=DEV)
+    k, v = (torch.full((Hkv, N, d), 7.0, dtype=od, device=DEV) for _ in range(2))
+    assert la.lib().la_kv4_read(c, N, cu.data_ptr(), start.data_ptr(), k.data_ptr(), v.data_ptr(), getattr(la, dtype),
+                                torch.cuda.current_stream().cuda_stream) == la.LA_OK
+    assert (k == 0).all() and (v == 0).all()
+
+
 # ------------------------------------------------------------------ decode
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,H", [(torch.float16, 4), (torch.bfloat16, 4), (torch.bfloat16, 12), (torch.float32, 4)])
