@@ -452,7 +452,7 @@ size_t la_kv4_decode_workspace_size(int B, int H, int H_kv, int cap, int d, int 
  *   0 <= recent <= keep, keep >= 1
  *   out_weights  [B, H_kv, out->cap] fp32 or NULL: the kept positions' weights
  *   kept         [B, H_kv, keep] int32 or NULL: their old positions, -1 behind them
- *   out_lens     [B] int32 or NULL: min(lens[b], keep)
+ *   out_lens     [B] int32 or NULL: min(lens[b], keep); refused without a head
  * No output may overlap weights or lens.
  */
 la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const int32_t *lens, int keep,

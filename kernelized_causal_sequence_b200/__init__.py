@@ -666,6 +666,7 @@ def la_kv4_evict(cache, weights, lens, keep, recent=0, out=None, out_weights=Non
     _ints(lens, B, dev, "lens")
     _floats(weights, (B, Hk, cap), dev, "weights")
     _need(keep >= 1 and 0 <= recent <= keep, "keep >= 1, 0 <= recent <= keep")
+    _need(Hk > 0 or B == 0, "cache: at least one head")
     device = lens.device
     cap_out = keep
     if out is not None:

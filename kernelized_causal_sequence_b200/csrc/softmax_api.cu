@@ -326,7 +326,8 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     if (out->B != cache->B || out->H_kv != cache->H_kv || out->d != cache->d || keep < 1 || recent < 0 ||
         recent > keep || out->cap < keep)
         return LA_ERR_INVALID_ARG;
-    if (cache->B == 0 || cache->H_kv == 0) return LA_OK;
+    if (cache->B == 0) return LA_OK;
+    if (cache->H_kv == 0) return out_lens ? LA_ERR_INVALID_ARG : LA_OK;   // (a head's CTA writes them)
     if (!lens || !al4(lens) || !al4(kept) || !al4(out_lens) || !al16(out_weights)) return LA_ERR_INVALID_ARG;
     if (cache->cap > 0 && (!weights || !al16(weights))) return LA_ERR_INVALID_ARG;
     const void *src[4] = {cache->k_codes, cache->v_codes, cache->k_par, cache->v_par};

@@ -144,6 +144,15 @@ def test_evict_refuses_outputs_over_inputs(L):
     assert ev(ol=P(2)) == ev(lens=P(2, 8), ol=P(2)) == ev(kept=P(2)) == ev(kept=P(1, 16)) == INVALID
 
 
+def test_evict_lengths_need_a_head(L):
+    """The new lengths are written with the heads' results: without a head nobody writes them."""
+    def ev(ol, **kw):
+        return L.la_kv4_evict(ctypes.byref(cache(H_kv=0, **kw)), P(1), P(2), 10, 0, ctypes.byref(cache(20, H_kv=0, cap=12, **kw)),
+                              P(5), P(6), ol, None, 0, None)
+    assert ev(P(7)) == INVALID
+    assert ev(None) == ev(P(7), B=0) == la.LA_OK
+
+
 def test_python_checks():
     f = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)
     i = lambda n: torch.zeros(n, dtype=torch.int32)
