@@ -453,7 +453,7 @@ size_t la_kv4_decode_workspace_size(int B, int H, int H_kv, int cap, int d, int 
  *   out_weights  [B, H_kv, out->cap] fp32 or NULL: the kept positions' weights
  *   kept         [B, H_kv, keep] int32 or NULL: their old positions, -1 behind them
  *   out_lens     [B] int32 or NULL: min(lens[b], keep); refused without a head
- * No output may overlap weights or lens.
+ * No output, the workspace among them, may overlap an input or another output.
  */
 la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const int32_t *lens, int keep,
                        int recent, const la_kv4_cache *out, float *out_weights, int32_t *kept,

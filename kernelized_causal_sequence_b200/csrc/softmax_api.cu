@@ -69,7 +69,22 @@ inline size_t span(int heads, int N, int d, long hs, long ts, int es) {
 }
 inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + nb && y < x + na;
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+// The memory of one argument of a call (null or empty: none).
+struct Region {
+    const void *at;
+    size_t bytes;
+};
+// Whether a call's outputs overlap its inputs or one another: CTAs write while others read.
+template <int NO, int NI> bool aliased(const Region (&out)[NO], const Region (&in)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes)) return true;
+    }
+    return false;
 }
 
 la_status check_cache(const la_kv4_cache *c) {
@@ -330,24 +345,17 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     if (cache->H_kv == 0) return out_lens ? LA_ERR_INVALID_ARG : LA_OK;   // (a head's CTA writes them)
     if (!lens || !al4(lens) || !al4(kept) || !al4(out_lens) || !al16(out_weights)) return LA_ERR_INVALID_ARG;
     if (cache->cap > 0 && (!weights || !al16(weights))) return LA_ERR_INVALID_ARG;
-    const void *src[4] = {cache->k_codes, cache->v_codes, cache->k_par, cache->v_par};
-    const void *dst[4] = {out->k_codes, out->v_codes, out->k_par, out->v_par};
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (overlap(src[i], i < 2 ? code_bytes(cache) : par_bytes(cache), dst[j],
-                        j < 2 ? code_bytes(out) : par_bytes(out)))
-                return LA_ERR_INVALID_ARG;
-    if (overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), out_weights,
-                (size_t)out->B * out->H_kv * out->cap * sizeof(float)))
-        return LA_ERR_INVALID_ARG;
-    // (a head's lengths are read while another's results are written)
-    const size_t lb = sizeof(int32_t) * (size_t)cache->B, kb = (size_t)cache->B * cache->H_kv * keep * sizeof(int32_t);
-    if (overlap(lens, lb, out_lens, lb) || overlap(lens, lb, kept, kb) ||
-        overlap(weights, (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float), kept, kb))
-        return LA_ERR_INVALID_ARG;
     // the list of kept positions: the caller's `kept`, or the workspace
     const size_t need = kept ? 0 : ws_up((size_t)cache->B * cache->H_kv * keep * sizeof(int32_t));
     if (!ws_ok(workspace, workspace_bytes, need)) return LA_ERR_INVALID_ARG;
+    const size_t heads = (size_t)cache->B * cache->H_kv, lb = sizeof(int32_t) * (size_t)cache->B;
+    const Region outs[] = {{out->k_codes, code_bytes(out)}, {out->k_par, par_bytes(out)}, {out->v_codes, code_bytes(out)},
+                           {out->v_par, par_bytes(out)}, {out_weights, heads * out->cap * sizeof(float)},
+                           {kept, heads * keep * sizeof(int32_t)}, {out_lens, lb}, {workspace, need}};
+    const Region ins[] = {{cache->k_codes, code_bytes(cache)}, {cache->k_par, par_bytes(cache)},
+                          {cache->v_codes, code_bytes(cache)}, {cache->v_par, par_bytes(cache)},
+                          {weights, heads * cache->cap * sizeof(float)}, {lens, lb}};
+    if (aliased(outs, ins)) return LA_ERR_INVALID_ARG;
     Kv4EvictParams p;
     std::memset(&p, 0, sizeof(p));
     p.c = dev_cache(cache); p.o = dev_cache(out); p.weights = weights; p.lens = lens; p.keep = keep;

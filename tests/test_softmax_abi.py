@@ -144,6 +144,40 @@ def test_evict_refuses_outputs_over_inputs(L):
     assert ev(ol=P(2)) == ev(lens=P(2, 8), ol=P(2)) == ev(kept=P(2)) == ev(kept=P(1, 16)) == INVALID
 
 
+def pairs(names, regions, given):
+    """Each (output, other) pair by name, with the output laid over the first and the last bytes of the other."""
+    for name in given:
+        for other in names:
+            if other != name:
+                at, n = regions[other]
+                yield name, other, at
+                yield name, other, at + n - 16
+
+
+# (bytes of the arrays of cache(): B 3, H_kv 2, cap 100, d 64)
+CACHE_BYTES = [600 * 32, 600 * 8, 600 * 32, 600 * 8]
+
+
+def test_evict_refuses_any_overlap(L):
+    """No output over an input or another output, first bytes or last, the workspace among them."""
+    size = dict(zip(("kc", "kp", "vc", "vp"), CACHE_BYTES), w=600 * 4, lens=16, okc=72 * 32, okp=72 * 8, ovc=72 * 32, ovp=72 * 8,
+                ow=72 * 4, kept=60 * 4, ol=16, ws=256)
+    place = {x: (P(i + 1).value, n) for i, (x, n) in enumerate(size.items())}
+    outputs = ["okc", "okp", "ovc", "ovp", "ow", "kept", "ol", "ws"]
+
+    def ev(**at):
+        a = {x: p for x, (p, _) in place.items()}
+        a.update(at)
+        kept = a["kept"] if "ws" not in at else None      # the workspace holds the list where `kept` is not given
+        return L.la_kv4_evict(ctypes.byref(la._Kv4CacheC(a["kc"], a["kp"], a["vc"], a["vp"], 3, 2, 100, 64)), a["w"], a["lens"],
+                              10, 0, ctypes.byref(la._Kv4CacheC(a["okc"], a["okp"], a["ovc"], a["ovp"], 3, 2, 12, 64)),
+                              a["ow"], kept, a["ol"], a["ws"], 256, None)
+    names = [x for x in size if x != "ws"]
+    wrong = [(o, x) for o, x, at in pairs(names, place, outputs)
+             if not (o == "ws" and (x == "kept" or at % 256)) and ev(**{o: at}) != INVALID]
+    assert not wrong
+
+
 def test_evict_lengths_need_a_head(L):
     """The new lengths are written with the heads' results: without a head nobody writes them."""
     def ev(ol, **kw):
