@@ -419,11 +419,13 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
  * cache's first lens[b] positions (lens [B] int32, device, clamped to
  * [0, cap]; a length of 0 gives zeros):
  *   out[b,h] = sum_t p_t V[b,h',t],  p = softmax_t(scale q[b,h].K[b,h',t])
- *   q, out  [B, H, d] contiguous; out must not overlap q
+ *   q, out  [B, H, d] contiguous
  *   weights_out  [B, H_kv, cap] fp32 or NULL: for t < lens[b] receives
  *           weights_in (zeros if NULL) + the sum of p_t over the query heads
  *           of that key/value head; the other entries are left as they were.
- *           May be weights_in itself; must not overlap it otherwise.
+ *           May be weights_in itself.
+ * Otherwise no output, the workspace among them, may overlap an input or
+ * another output.
  * The products run on the tensor cores in fp16 terms, scaled by powers of two:
  * 4-bit codes and 16-bit queries are exact there; the weights times the
  * values' scales are rounded once to fp16's 11 bits (16-bit queries) or carried

@@ -305,12 +305,15 @@ la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_ca
     if (H == 0 || cache->B == 0) return LA_OK;
     if (!q || !lens || !out || !al16(q) || !al16(out) || !al4(lens) || !al16(weights_in) || !al16(weights_out))
         return LA_ERR_INVALID_ARG;
-    const size_t elems = (size_t)cache->B * H * cache->d;
-    if (overlap(out, elems * esize(out_dtype), q, elems * esize(in_dtype))) return LA_ERR_INVALID_ARG;
-    const size_t wb = (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float);
-    if (weights_in != weights_out && overlap(weights_in, wb, weights_out, wb)) return LA_ERR_INVALID_ARG;
     const DecodePlan pl = decode_plan(cache->B, H, cache->H_kv, cache->cap, cache->d, weights_out != nullptr);
     if (!ws_ok(workspace, workspace_bytes, pl.bytes)) return LA_ERR_INVALID_ARG;
+    const size_t elems = (size_t)cache->B * H * cache->d, wb = (size_t)cache->B * cache->H_kv * cache->cap * sizeof(float);
+    const Region outs[] = {{out, elems * esize(out_dtype)}, {weights_out, wb}, {workspace, pl.bytes}};
+    const Region ins[] = {{q, elems * esize(in_dtype)}, {lens, sizeof(int32_t) * (size_t)cache->B},
+                          {weights_in == weights_out ? nullptr : weights_in, wb},
+                          {cache->k_codes, code_bytes(cache)}, {cache->k_par, par_bytes(cache)},
+                          {cache->v_codes, code_bytes(cache)}, {cache->v_par, par_bytes(cache)}};
+    if (aliased(outs, ins)) return LA_ERR_INVALID_ARG;
     if ((long)cache->B * cache->H_kv * pl.head_blocks > 0x7fffffffL) return LA_ERR_UNSUPPORTED;
     char *ws = (char *)workspace;
     Kv4DecodeParams p;

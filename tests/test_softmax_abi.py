@@ -178,6 +178,23 @@ def test_evict_refuses_any_overlap(L):
     assert not wrong
 
 
+def test_decode_refuses_any_overlap(L):
+    """No output over an input or another output, the workspace among them; weights_in may be weights_out."""
+    need = la.la_kv4_decode_workspace_size(3, 4, 2, 100, 64, True)
+    size = dict(zip(("kc", "kp", "vc", "vp"), CACHE_BYTES), q=12 * 128, lens=16, wi=600 * 4, wo=600 * 4, out=12 * 128, ws=need)
+    place = {x: (P(i + 1).value, n) for i, (x, n) in enumerate(size.items())}
+
+    def dec(**at):
+        a = {x: p for x, (p, _) in place.items()}
+        a.update(at)
+        c = la._Kv4CacheC(a["kc"], a["kp"], a["vc"], a["vp"], 3, 2, 100, 64)
+        return L.la_kv4_decode(a["q"], la.LA_BF16, 4, ctypes.byref(c), a["lens"], 0.1, a["wi"], a["wo"], a["out"], la.LA_BF16,
+                               a["ws"], need, None)
+    wrong = [(o, x) for o, x, at in pairs(size, place, ["out", "wo", "ws"])
+             if not (o == "ws" and at % 256) and not (o == "wo" and x == "wi" and at == place["wi"][0]) and dec(**{o: at}) != INVALID]
+    assert not wrong
+
+
 def test_evict_lengths_need_a_head(L):
     """The new lengths are written with the heads' results: without a head nobody writes them."""
     def ev(ol, **kw):
