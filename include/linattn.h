@@ -401,6 +401,7 @@ typedef struct {
  *   k, v   [H_kv, N, d] in_dtype; strides: 4 entries (k, v)
  *   start  [B] int32, device
  * Two tokens never share a position of one call; the cache keeps no lengths.
+ * The cache's arrays must not overlap the inputs or one another.
  */
 la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, const int64_t *strides,
                         const int32_t *cu_seqlens, const int32_t *start, const la_kv4_cache *cache,
@@ -409,7 +410,8 @@ la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, 
 /*
  * la_kv4_read — the inverse: the values of positions start[s] + (t -
  * cu_seqlens[s]), as k_out, v_out [H_kv, N, d] out_dtype, contiguous.
- * Positions outside [0, cap) and tokens of no sequence give zeros.
+ * Positions outside [0, cap) and tokens of no sequence give zeros.  The outputs
+ * must not overlap the inputs or each other.
  */
 la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlens, const int32_t *start,
                       void *k_out, void *v_out, la_dtype out_dtype, void *stream);

@@ -259,6 +259,12 @@ la_status la_kv4_append(const void *k, const void *v, la_dtype in_dtype, int N, 
         return LA_ERR_INVALID_ARG;
     if (N == 0 || cache->B == 0 || cache->H_kv == 0 || cache->cap == 0) return LA_OK;
     if (!k || !v || !start || !al16(k) || !al16(v) || !al4(start) || !al4(cu_seqlens)) return LA_ERR_INVALID_ARG;
+    const Region outs[] = {{cache->k_codes, code_bytes(cache)}, {cache->k_par, par_bytes(cache)},
+                           {cache->v_codes, code_bytes(cache)}, {cache->v_par, par_bytes(cache)}};
+    const Region ins[] = {{k, span(cache->H_kv, N, cache->d, p.k_hs, p.k_ts, es)},
+                          {v, span(cache->H_kv, N, cache->d, p.v_hs, p.v_ts, es)},
+                          {cu_seqlens, sizeof(int32_t) * ((size_t)cache->B + 1)}, {start, sizeof(int32_t) * (size_t)cache->B}};
+    if (aliased(outs, ins)) return LA_ERR_INVALID_ARG;
     p.k = k; p.v = v; p.cu = cu_seqlens; p.start = start; p.c = dev_cache(cache); p.N = N;
     cudaStream_t st = (cudaStream_t)stream;
     if (in_dtype == LA_F32) return run_append<float>(p, cache->d, st);
@@ -275,8 +281,13 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
     if (N == 0 || cache->H_kv == 0) return LA_OK;
     if (!k_out || !v_out || !al16(k_out) || !al16(v_out) || (cache->B && !start) || !al4(start) || !al4(cu_seqlens))
         return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)cache->H_kv * N * cache->d * esize(out_dtype);
+    const Region outs[] = {{k_out, n}, {v_out, n}};
+    const Region ins[] = {{cache->k_codes, code_bytes(cache)}, {cache->k_par, par_bytes(cache)},
+                          {cache->v_codes, code_bytes(cache)}, {cache->v_par, par_bytes(cache)},
+                          {cu_seqlens, sizeof(int32_t) * ((size_t)cache->B + 1)}, {start, sizeof(int32_t) * (size_t)cache->B}};
+    if (aliased(outs, ins)) return LA_ERR_INVALID_ARG;
     if (cache->B == 0) {   // tokens of no sequence
-        const size_t n = (size_t)cache->H_kv * N * cache->d * esize(out_dtype);
         if ((s = cuda_check("kv4 read", cudaMemsetAsync(k_out, 0, n, (cudaStream_t)stream))) != LA_OK) return s;
         return cuda_check("kv4 read", cudaMemsetAsync(v_out, 0, n, (cudaStream_t)stream));
     }

@@ -195,6 +195,24 @@ def test_decode_refuses_any_overlap(L):
     assert not wrong
 
 
+def test_append_read_refuse_any_overlap(L):
+    """No cache array over an input or another array in an append, no output over the cache, the indexes or the other
+    output in a read."""
+    size = dict(zip(("kc", "kp", "vc", "vp"), CACHE_BYTES), k=2 * 50 * 128, v=2 * 50 * 128, cu=16, start=16)
+    place = {x: (P(i + 1).value, n) for i, (x, n) in enumerate(size.items())}
+
+    def call(which, **at):
+        a = {x: p for x, (p, _) in place.items()}
+        a.update(at)
+        c = ctypes.byref(la._Kv4CacheC(a["kc"], a["kp"], a["vc"], a["vp"], 3, 2, 100, 64))
+        if which == "append":
+            return L.la_kv4_append(a["k"], a["v"], la.LA_BF16, 50, None, a["cu"], a["start"], c, None)
+        return L.la_kv4_read(c, 50, a["cu"], a["start"], a["k"], a["v"], la.LA_BF16, None)
+    wrong = [("append", o, x) for o, x, at in pairs(size, place, ["kc", "kp", "vc", "vp"]) if call("append", **{o: at}) != INVALID]
+    wrong += [("read", o, x) for o, x, at in pairs(size, place, ["k", "v"]) if call("read", **{o: at}) != INVALID]
+    assert not wrong
+
+
 def test_evict_lengths_need_a_head(L):
     """The new lengths are written with the heads' results: without a head nobody writes them."""
     def ev(ol, **kw):
