@@ -345,7 +345,7 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  *   p_ij = exp(scale q_i.k_j) / sum_{j' <= i} exp(scale q_i.k_j')
  *   q, out [H, N, d], k, v [H_kv, N, d]; strides: 8 entries (q, k, v, out)
  *   scale  finite and > 0
- *   out    must not overlap the inputs
+ *   out    and the workspace must not overlap the inputs or each other
  * Keys and values behind a query, or of another sequence, do not reach it,
  * not even as NaN or infinity.  Sums and the running maximum are fp32; with
  * 16-bit inputs (the tensor-core kernel) the unnormalised weights are rounded

@@ -225,13 +225,11 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
     if (H == 0 || N == 0 || n_seq == 0) return LA_OK;
     if (!q || !k || !v || !out || !cu_seqlens || !al16(q) || !al16(k) || !al16(v) || !al16(out) || !al4(cu_seqlens))
         return LA_ERR_INVALID_ARG;
-    const size_t os = span(H, N, d, p.o_hs, p.o_ts, oe);
-    if (overlap(out, os, q, span(H, N, d, p.q_hs, p.q_ts, ie)) ||
-        overlap(out, os, k, span(H_kv, N, d, p.k_hs, p.k_ts, ie)) ||
-        overlap(out, os, v, span(H_kv, N, d, p.v_hs, p.v_ts, ie)) ||
-        overlap(out, os, cu_seqlens, sizeof(int32_t) * ((size_t)n_seq + 1)))
-        return LA_ERR_INVALID_ARG;
     if (!ws_ok(workspace, workspace_bytes, kWsAlign)) return LA_ERR_INVALID_ARG;
+    const Region outs[] = {{out, span(H, N, d, p.o_hs, p.o_ts, oe)}, {workspace, kWsAlign}};
+    const Region ins[] = {{q, span(H, N, d, p.q_hs, p.q_ts, ie)}, {k, span(H_kv, N, d, p.k_hs, p.k_ts, ie)},
+                          {v, span(H_kv, N, d, p.v_hs, p.v_ts, ie)}, {cu_seqlens, sizeof(int32_t) * ((size_t)n_seq + 1)}};
+    if (aliased(outs, ins)) return LA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     p.q = q; p.k = k; p.v = v; p.out = out; p.cu = cu_seqlens;
     p.H = H; p.group = H / H_kv; p.N = N; p.n_seq = n_seq;

@@ -68,6 +68,13 @@ def test_prefill_nothing_to_do(L):
     assert la.la_softmax_prefill_workspace_size(8, 2, 100, 80, 1) == 0
 
 
+def test_prefill_refuses_a_workspace_over_its_arrays(L):
+    """The call sets the workspace's first words before it reads the others."""
+    for kw in (dict(ws=P(1)), dict(ws=P(2)), dict(ws=P(3)), dict(ws=P(4)), dict(ws=P(5)), dict(ws=P(1, 8 * 1000 * 256 - 256)),
+               dict(ws=P(5, 8 * 1000 * 256 - 256)), dict(out=P(4))):
+        assert prefill(L, **kw) == INVALID
+
+
 def cache(i=10, **kw):
     a = dict(k_codes=P(i), k_par=P(i + 1), v_codes=P(i + 2), v_par=P(i + 3), B=3, H_kv=2, cap=100, d=64)
     a.update(kw)
