@@ -344,7 +344,7 @@ la_status la_decode_step_mlstm(const void *q, const void *k, const void *v, la_d
  *   out_i = sum_{j <= i, same sequence} p_ij v_j,
  *   p_ij = exp(scale q_i.k_j) / sum_{j' <= i} exp(scale q_i.k_j')
  *   q, out [H, N, d], k, v [H_kv, N, d]; strides: 8 entries (q, k, v, out)
- *   scale  finite and > 0
+ *   scale  > 0, scale log2(e) a normal fp32 number
  *   out    and the workspace must not overlap the inputs or each other
  * Keys and values behind a query, or of another sequence, do not reach it,
  * not even as NaN or infinity.  Sums and the running maximum are fp32; with
@@ -419,7 +419,7 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
 /*
  * la_kv4_decode — softmax attention of one query token per sequence over the
  * cache's first lens[b] positions (lens [B] int32, device, clamped to
- * [0, cap]; a length of 0 gives zeros):
+ * [0, cap]; a length of 0 gives zeros; scale as above):
  *   out[b,h] = sum_t p_t V[b,h',t],  p = softmax_t(scale q[b,h].K[b,h',t])
  *   q, out  [B, H, d] contiguous
  *   weights_out  [B, H_kv, cap] fp32 or NULL: for t < lens[b] receives

@@ -30,6 +30,10 @@ inline bool ws_ok(const void *ws, size_t have, size_t need) {
     return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) == 0);
 }
 
+// What the kernels multiply scores by: scale log2(e), a normal number (an infinite one makes a score of 0 NaN, a
+// subnormal one is cut short).
+inline bool scale_ok(float scale) { return scale > 0.f && std::isnormal(scale * kLog2e); }
+
 la_status check_types(la_dtype in, la_dtype out, int d) {
     if (!dt_ok(in) || !dt_ok(out) || d <= 0) return LA_ERR_INVALID_ARG;
     if (!d_ok(d) || !(out == in || out == LA_F32)) return LA_ERR_UNSUPPORTED;
@@ -213,7 +217,7 @@ la_status la_softmax_prefill(const void *q, const void *k, const void *v, la_dty
                              size_t workspace_bytes, void *stream) {
     la_status s = check_types(in_dtype, out_dtype, d);
     if (s != LA_OK || (s = check_heads(H, H_kv)) != LA_OK) return s;
-    if (N < 0 || n_seq < 0 || !(std::isfinite(scale) && scale > 0.f)) return LA_ERR_INVALID_ARG;
+    if (N < 0 || n_seq < 0 || !scale_ok(scale)) return LA_ERR_INVALID_ARG;
     if (N > kMaxTokens || n_seq > kMaxTokens) return LA_ERR_UNSUPPORTED;
     SoftmaxParams p;
     const int ie = esize(in_dtype), oe = esize(out_dtype);
@@ -310,7 +314,7 @@ la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_ca
     if (s != LA_OK || (s = check_types(in_dtype, out_dtype, cache->d)) != LA_OK ||
         (s = check_heads(H, cache->H_kv)) != LA_OK)
         return s;
-    if (!(std::isfinite(scale) && scale > 0.f) || (weights_in && !weights_out)) return LA_ERR_INVALID_ARG;
+    if (!scale_ok(scale) || (weights_in && !weights_out)) return LA_ERR_INVALID_ARG;
     if (H == 0 || cache->B == 0) return LA_OK;
     if (!q || !lens || !out || !al16(q) || !al16(out) || !al4(lens) || !al16(weights_in) || !al16(weights_out))
         return LA_ERR_INVALID_ARG;

@@ -75,6 +75,14 @@ def test_prefill_refuses_a_workspace_over_its_arrays(L):
         assert prefill(L, **kw) == INVALID
 
 
+@pytest.mark.parametrize("scale,ok", [(1e-45, False), (1e-39, False), (2e-38, True), (2.3e38, True), (2.4e38, False), (3.4e38, False)])
+def test_scale_range(L, scale, ok):
+    """scale log2(e), which the kernels multiply by, has to be a normal number: neither cut short nor infinite."""
+    want = la.LA_OK if ok else INVALID
+    assert prefill(L, scale=scale, N=0) == want
+    assert L.la_kv4_decode(P(1), la.LA_BF16, 0, ctypes.byref(cache(H_kv=0)), P(2), scale, None, None, P(3), la.LA_BF16, P(4), 256, None) == want
+
+
 def cache(i=10, **kw):
     a = dict(k_codes=P(i), k_par=P(i + 1), v_codes=P(i + 2), v_par=P(i + 3), B=3, H_kv=2, cap=100, d=64)
     a.update(kw)
