@@ -11,7 +11,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_softmax_ops import DEV, U, U32, check_prefill, cu_of, fill_cache, pack_ref, prefill_inputs, ref_evict, tensor_cores
+from test_softmax_ops import (DEV, U, U32, check_prefill, cu_of, fill_cache, pack_ref, prefill_inputs, ref_decode,
+                              ref_evict, tensor_cores)
 
 
 def i32(*x):
@@ -80,6 +81,23 @@ def test_prefill_one_key_takes_the_weight(la, dtype, d, H, Hkv, bits, at):
     k[:, at], v[:, at] = 0, 0
     out = la.la_softmax_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([n]), scale=1.0, out_dtype=torch.float32)
     check_prefill(out[:1], q[:1], k[:1], v[:1], [n], 1.0, tensor_cores(dtype, d))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,H,Hkv,n", [(torch.float32, 64, 6, 2, 333), (torch.float32, 128, 4, 4, 70), (torch.float32, 32, 64, 8, 333),
+                                             (torch.float16, 32, 6, 2, 333)])
+def test_prefill_views_of_a_projection(la, dtype, d, H, Hkv, n):
+    """q, k, v as views of one token-major projection with a gap behind each token, out token-major."""
+    lens = [n // 3, n - n // 3]
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, (H + 2 * Hkv + 1) * d, generator=g).to(dtype).to(DEV)
+    heads = x.view(n, H + 2 * Hkv + 1, d).transpose(0, 1)
+    q, k, v = heads[:H], heads[H:H + Hkv], heads[H + Hkv:H + 2 * Hkv]
+    out = torch.zeros(n, H, d, dtype=dtype, device=DEV)
+    la.la_softmax_prefill(q, k, v, cu_of(lens), out=out.transpose(0, 1))
+    want = la.la_softmax_prefill(q.contiguous(), k.contiguous(), v.contiguous(), cu_of(lens))
+    assert torch.equal(out.transpose(0, 1), want)
+    check_prefill(want, q.cpu(), k.cpu(), v.cpu(), lens, d ** -0.5, tensor_cores(dtype, d))
 
 
 # ------------------------------------------------------------------ reading back
@@ -154,6 +172,70 @@ def test_decode_cache_without_positions(la, H, with_weights):
     assert (out == 0).all() and (w == 5.0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("H", [1, 4, 12])
+@pytest.mark.parametrize("T", [2, 32])
+def test_decode_rounding_of_the_weights(la, dtype, d, H, T):
+    """The weights times scales are rounded to fp16's 11 bits whatever the 16-bit type of the queries, or carried as
+    two such terms (fp32 queries; one value row of the T is not 0 then, so that no sum covers the rounding).
+
+    Bound.  As in test_decode_one_position_takes_the_weight, with no weight below 2^-3 of another's.  A sum of r rows
+    in one tile takes at most r products, r offsets and 8 more roundings, each of a number below 31 scales."""
+    g = torch.Generator().manual_seed(T + d + H)
+    q = torch.zeros(1, H, d, dtype=dtype)
+    q[0, :, 0] = 1 + torch.arange(H) / 32
+    k = torch.zeros(1, 1, T, d)
+    k[..., 0] = 2 * torch.rand(1, 1, T, generator=g) - 1
+    v = torch.randn(1, 1, T, d, generator=g)
+    rows = T
+    if dtype == torch.float32:
+        v[:, :, 1:], rows = 0, 1
+    cache, kv, vv = fill_cache(la, k, v)
+    out = la.la_kv4_decode(q.to(DEV), cache, i32(T), scale=1.0, out_dtype=torch.float32)[0].double().cpu()
+    vs = torch.from_numpy(pack_ref(v)[1])[0, 0].repeat_interleave(32, -1)
+    ks = float(torch.from_numpy(pack_ref(k)[1]).max())
+    for h in range(H):
+        s = kv[0, 0, :, 0] * q[0, h, 0].double()
+        p = torch.softmax(s, 0)
+        ref, A = p @ vv[0, 0], p @ vv[0, 0].abs()
+        rel = 2 * (8 * U32 * 2 * 31 * ks + 4 * U32 * float(s.abs().max())) + 2 * 2.0 ** -20 + 2 * (T + 8) * U32
+        tol = rel * A + (2 * rows + 8) * U32 * 31 * (p @ vs) + U32 * ref.abs() + 1e-30
+        tol = tol + (2.0 ** -22 if dtype == torch.float32 else U[torch.float16]) * A
+        assert float(((out[h] - ref).abs() / tol).max()) <= 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,H,Hkv", [(torch.bfloat16, 64, 4, 1), (torch.float16, 32, 20, 1), (torch.float32, 32, 4, 2),
+                                           (torch.bfloat16, 128, 2, 2)])
+def test_decode_lengths_of_every_size(la, dtype, d, H, Hkv):
+    """Forty sequences from none to thousands of positions in one cut line: each as if it were alone, the weights too,
+    and every run with the same bits."""
+    T, B = 3000, 40
+    rng = np.random.default_rng(d)
+    lens = [0, 1, 2, 31, 32, 33, 0, T, T - 1, 2049] + [int(x) for x in np.exp(rng.uniform(0, math.log(T), B - 10))]
+    rng.shuffle(lens)
+    g = torch.Generator().manual_seed(d)
+    k, v = torch.randn(B, Hkv, T, d, generator=g), torch.randn(B, Hkv, T, d, generator=g)
+    q = torch.randn(B, H, d, generator=g).to(dtype)
+    cache, kv, vv = fill_cache(la, k, v)
+    ref, tol, A, w, wtol = ref_decode(q, kv, vv, lens, d ** -0.5, torch.from_numpy(pack_ref(v)[1]))
+    tol = tol + (U[torch.float16] if dtype != torch.float32 else 2.0 ** -22) * A
+    tol = tol + U[dtype] * (ref.abs() + tol) + 1e-30
+    cap = cache.k_codes.shape[2]
+    runs = []
+    for _ in range(3):
+        wo = torch.full((B, Hkv, cap), 5.0, device=DEV)
+        runs.append((la.la_kv4_decode(q.to(DEV), cache, i32(*lens), weights_out=wo), wo))
+        assert torch.equal(runs[-1][0], runs[0][0]) and torch.equal(wo, runs[0][1])
+    assert torch.equal(la.la_kv4_decode(q.to(DEV), cache, i32(*lens)), runs[0][0])
+    assert float(((runs[0][0].double().cpu() - ref).abs() / tol).max()) <= 1.0
+    for b, n in enumerate(lens):
+        assert ((runs[0][1][b, :, :n].cpu().double() - w[b, :, :n]).abs() <= wtol[b, :, :n] + 4 * U32 * w[b, :, :n] + 1e-30).all()
+        assert (runs[0][1][b, :, n:] == 5.0).all()
+
+
 # ------------------------------------------------------------------ eviction
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,Hkv,cap,lens,keep,recent", [
@@ -184,3 +266,31 @@ def test_evict_clusters_with_nothing_to_choose(la, d, Hkv, cap, lens, keep, rece
                 assert ow[b, h, :m].tolist() == w[b, h, want].tolist() and (ow[b, h, m:] == 0).all()
                 for x, y in zip(c, out):
                     assert torch.equal(y[b, h, :m], x[b, h, want])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap,lens,keep,recent", [(300, [300, 7, 0], 64, 10), (20000, [20000, 9000], 4000, 100)])
+def test_evict_without_optional_outputs(la, cap, lens, keep, recent):
+    """The rows are the same whichever of the other outputs are asked for (without `kept` the workspace holds the list)."""
+    B, Hkv, d = len(lens), 2, 64
+    rng = np.random.default_rng(cap)
+    c = la.KV4Cache.alloc(B, Hkv, cap, d, DEV)
+    for x in c:
+        x.view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 256, size=tuple(x.view(torch.uint8).shape), dtype=np.uint8)))
+    w = torch.from_numpy(rng.random((B, Hkv, cap)).astype(np.float32)).to(DEV)
+    want, kept, ow, ol = la.la_kv4_evict(c, w, i32(*lens), keep, recent=recent)
+    ws = torch.empty(la.la_kv4_evict_workspace_size(B, Hkv, cap, keep), dtype=torch.uint8, device=DEV)
+    for asked in range(8):
+        out = la.KV4Cache.alloc(B, Hkv, keep, d, DEV)
+        got = [torch.empty_like(kept), torch.zeros_like(ow), torch.empty_like(ol)]
+        at = [x.data_ptr() if asked >> i & 1 else None for i, x in enumerate(got)]
+        lens_d = i32(*lens)
+        assert la.lib().la_kv4_evict(la._cache_c(c)[0], w.data_ptr(), lens_d.data_ptr(), keep, recent, la._cache_c(out)[0], at[1], at[0],
+                                     at[2], ws.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream) == la.LA_OK
+        for b in range(B):
+            m = min(lens[b], keep)
+            for x, y in zip(out, want):
+                assert torch.equal(x[b, :, :m], y[b, :, :m])
+        for i, y in enumerate((kept, ow, ol)):
+            if asked >> i & 1:
+                assert torch.equal(got[i], y)
