@@ -48,7 +48,7 @@
 // walks its piece row by row, its warps take turns at the tiles and join at
 // the row's end; a row cut between CTAs is joined by kv4_finish_kernel.
 // Short caches are dealt out by whole rows instead and need no second kernel
-// (16 x 16 rows, lengths to 2048 at d 64: 18.0 / 16.5 us).
+// (kDecWhole).
 //
 // What bounds it.  64 sequences of up to 8192 positions, 16 heads on 4, d 128,
 // bf16: 55 us for 168 MB (26 us at the copy rate); the integer pipe is 54% busy
@@ -85,8 +85,14 @@ constexpr int kDecCtas = 3;         // CTAs per SM with up to 8 query heads (mor
 constexpr int kDecMinTiles = 16;    // places of a CTA at least: three or four tiles a warp, to hide its start
 constexpr int kDecRowCost = 8;      // tiles' worth of time (of four warps) that a row's start and join take
                                     // (64 rows x 4, lengths to 8192: 0 66.9 us, 4 64.5, 8 63.9, 12 64.0)
-constexpr int kDecWhole = 512, kDecWholeFull = 2048;   // positions up to which a row is not cut: always, and
-                                                       // where there is a row for every SM
+// Positions (of the cache: the lengths are on the device) up to which a row is not cut: always, and where there is a
+// row for every SM.  us whole / cut, all rows full (lengths spread evenly), weights in the first two lines:
+//   4 rows, d 128, bf16      700: 16 / 18 (10 / 18), 1024: 18 / 18 (16 / 20), 1300: 25 / 18 (12 / 16)
+//   120 rows, d 128, fp16    700: 20 / 25 (18 / 23), 1024: 27 / 27 (20 / 25), 1300: 31 / 29 (27 / 25)
+//   4 rows, d 128, bf16      2048: 25 / 18 (18 / 18), 4096: 41 / 18 (27 / 18)
+//   256 rows, d 64, fp16     1024: 16 / 22 (16 / 20), 2048: 25 / 29 (20 / 23), 4096: 39 / 43 (31 / 25)
+//   256 rows, d 128, bf16    1024: 23 / 33 (23 / 29), 2048: 37 / 45 (31 / 34), 4096: 62 / 66 (51 / 43)
+constexpr int kDecWhole = 1024, kDecWholeFull = 2048;
 
 // Row i of a 16-row tile holds this position of it: odd pairs are swapped, so
 // that rows 0, 2, 4, 6 (one value load of a warp) alternate between even and

@@ -207,6 +207,24 @@ def test_decode_rounding_of_the_weights(la, dtype, d, H, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1019, 1020])
+def test_decode_on_both_sides_of_whole_rows(la, T):
+    """Caches of 1024 and 1025 positions (whole rows and the cut line): right, and within rounding of each other."""
+    lens = [T, 700, 1]
+    g = torch.Generator().manual_seed(17)
+    k, v = (torch.randn(3, 2, 1020, 64, generator=g)[:, :, :T] for _ in range(2))
+    q = torch.randn(3, 6, 64, generator=g).to(torch.bfloat16)
+    cache, kv, vv = fill_cache(la, k, v)
+    assert cache.k_codes.shape[2] == T + 5
+    wo = torch.zeros(3, 2, T + 5, device=DEV)
+    out = la.la_kv4_decode(q.to(DEV), cache, i32(*lens), weights_out=wo, out_dtype=torch.float32)
+    ref, tol, A, w, wtol = ref_decode(q, kv, vv, lens, 0.125, torch.from_numpy(pack_ref(v)[1]))
+    tol = tol + U[torch.float16] * A + U32 * ref.abs() + 1e-30
+    assert float(((out.double().cpu() - ref).abs() / tol).max()) <= 1.0
+    assert ((wo.cpu().double()[:, :, :T] - w).abs() <= wtol + 4 * U32 * w + 1e-30).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,H,Hkv", [(torch.bfloat16, 64, 4, 1), (torch.float16, 32, 20, 1), (torch.float32, 32, 4, 2),
                                            (torch.bfloat16, 128, 2, 2)])
 def test_decode_lengths_of_every_size(la, dtype, d, H, Hkv):
