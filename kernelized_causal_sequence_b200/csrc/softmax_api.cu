@@ -134,8 +134,11 @@ template <int BM> la_status run_softmax_simt_bm(const SoftmaxParams &p, int d, c
                                     softmax_simt_smem<D, BM>(), st, true, "softmax prefill launch", p))
 }
 la_status run_softmax_simt(const SoftmaxParams &p, int d, cudaStream_t st) {
-    // tiles of 64 queries fill the machine, or tiles of 16 for more CTAs
-    if ((long)seq_tiles(p.N, p.n_seq, 64) * p.H >= kNumSMs) return run_softmax_simt_bm<64>(p, d, st);
+    // tiles of 64 queries, or of 16 where those leave half of the SMs without one (us 16 / 64, tiles of 64 over all heads:
+    //   d 64   1 x 320, 8 heads (48): 37 / 41, 2 x 256, 8 heads (80): 39 / 35, 1 x 1024, 8 heads (136): 162 / 111
+    //   d 128  1 x 128, 16 heads (48): 27 / 33, 1 x 256 (80): 66 / 51, 1 x 320 (96): 83 / 61
+    // of many sequences shorter than a tile 16 stay faster: 16 x 16 tokens, d 64, 16 heads (320): 14 / 16)
+    if (2L * seq_tiles(p.N, p.n_seq, 64) * p.H >= kNumSMs) return run_softmax_simt_bm<64>(p, d, st);
     return run_softmax_simt_bm<16>(p, d, st);
 }
 template <typename InT> la_status run_append(const Kv4AppendParams &p, int d, cudaStream_t st) {

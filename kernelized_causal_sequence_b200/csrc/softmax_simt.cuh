@@ -2,8 +2,8 @@
 // CUDA cores, for fp32 inputs (whose 1e-4 class the 16-bit tensor-core operands
 // cannot meet).
 //
-// One CTA takes BM queries of one head (64, or 16 where 64 would leave most SMs
-// without work) and walks the keys up to its last query in tiles of 64, keeping
+// One CTA takes BM queries of one head (64, or 16 where 64 would leave half of
+// the SMs without work) and walks the keys up to its last query in tiles of 64, keeping
 // for each row the running maximum m, the sum l and the unnormalised output o
 // (all fp32):
 //   m' = max(m, max_j s_j),  l' = l 2^(m - m') + sum_j 2^(s_j - m'),

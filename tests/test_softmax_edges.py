@@ -84,6 +84,19 @@ def test_prefill_one_key_takes_the_weight(la, dtype, d, H, Hkv, bits, at):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("H,Hkv", [(3, 1), (16, 4)])
+def test_prefill_fp32_tiles(la, d, H, Hkv):
+    """Tiles of 16 queries (few heads) and of 64, over sequences that end on, before and behind a tile's end."""
+    lens = [64, 0, 1, 200, 63, 65, 16, 17, 15, 129]
+    q, k, v = prefill_inputs(torch.float32, d, H, Hkv, sum(lens) + 2, seed=d + H)
+    out = torch.full_like(q, 7.0, device=DEV)
+    la.la_softmax_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu_of(lens), out=out)
+    assert (out[:, sum(lens):] == 7.0).all()
+    check_prefill(out, q, k, v, lens, d ** -0.5, False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,H,Hkv,n", [(torch.float32, 64, 6, 2, 333), (torch.float32, 128, 4, 4, 70), (torch.float32, 32, 64, 8, 333),
                                              (torch.float16, 32, 6, 2, 333)])
 def test_prefill_views_of_a_projection(la, dtype, d, H, Hkv, n):
