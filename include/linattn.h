@@ -433,7 +433,8 @@ la_status la_kv4_read(const la_kv4_cache *cache, int N, const int32_t *cu_seqlen
  * values' scales are rounded once to fp16's 11 bits (16-bit queries) or carried
  * as two terms, like fp32 queries: relative to themselves, down to 2^-26 of the
  * greatest weight times the largest scale, and below that to a multiple of
- * 2^-36 of it (the second of two terms too).  Sums are fp32.
+ * 2^-36 of it (the second of two terms too).  Sums are fp32.  Keys may be
+ * as large as 2^100 (the queries' scaling takes its part of fp32's range).
  */
 la_status la_kv4_decode(const void *q, la_dtype in_dtype, int H, const la_kv4_cache *cache, const int32_t *lens,
                         float scale, const float *weights_in, float *weights_out, void *out,
@@ -469,9 +470,9 @@ size_t la_kv4_evict_workspace_size(int B, int H_kv, int cap, int keep);
 
 /*
  * Status of the last call that used `workspace` (a workspace passed to
- * la_prefill_causal*, la_forward_noncausal or la_prefill_causal_noalloc's
- * array): LA_OK, or LA_ERR_TIMEOUT if a bounded device-side wait of that call
- * gave up (its output and state are then incomplete).  *waiter (if non-NULL)
+ * la_prefill_causal*, la_forward_noncausal, la_softmax_prefill or
+ * la_prefill_causal_noalloc's array): LA_OK, or LA_ERR_TIMEOUT if a bounded
+ * device-side wait of that call gave up (its output and state are then incomplete).  *waiter (if non-NULL)
  * receives the id of the first wait that gave up (0 if none), for diagnosis.
  * Unlike every other entry point this one synchronises `stream`: it copies
  * the 8-byte status word to the host on `stream` and waits for it.  Call it on

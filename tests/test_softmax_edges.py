@@ -220,6 +220,22 @@ def test_decode_rounding_of_the_weights(la, dtype, d, H, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("power", [-99, 99])
+def test_decode_ranges_of_keys_and_queries(la, dtype, power):
+    """Keys of 2^99 under queries of 2^-99, and the other way round: ordinary scores."""
+    T, d = 300, 128
+    g = torch.Generator().manual_seed(19)
+    k, v = torch.randn(1, 1, T, d, generator=g), torch.randn(1, 1, T, d, generator=g)
+    q = torch.randn(1, 4, d, generator=g).to(dtype)
+    cache, kv, vv = fill_cache(la, k * 2.0 ** power, v)
+    ref, tol, A, _, _ = ref_decode(q.double() * 2.0 ** -power, kv, vv, [T], d ** -0.5, torch.from_numpy(pack_ref(v)[1]))
+    out = la.la_kv4_decode((q * 2.0 ** -power).to(DEV), cache, i32(T), out_dtype=torch.float32)
+    tol = tol + (U[torch.float16] if dtype != torch.float32 else 2.0 ** -22) * A + U32 * ref.abs()
+    assert float(((out.double().cpu() - ref).abs() / tol).max()) <= 1.0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1019, 1020])
 def test_decode_on_both_sides_of_whole_rows(la, T):
     """Caches of 1024 and 1025 positions (whole rows and the cut line): right, and within rounding of each other."""
@@ -277,6 +293,8 @@ def test_decode_lengths_of_every_size(la, dtype, d, H, Hkv):
     (128, 1, 9000, [9000, 9000], 9000, 0),
     (32, 1, 70000, [70000, 3], 500, 500),
     (32, 1, 70000, [400, 0, 500, 70000], 500, 250),
+    # more rows than SMs: one small block each, to its last key
+    (32, 2, 2048, [2048, 2047, 0, 900] + [1300] * 76, 1000, 11),
 ])
 def test_evict_clusters_with_nothing_to_choose(la, d, Hkv, cap, lens, keep, recent):
     B = len(lens)
