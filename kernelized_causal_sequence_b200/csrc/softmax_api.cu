@@ -164,6 +164,8 @@ struct DecodePlan {
 DecodePlan decode_plan(int B, int H, int H_kv, int cap, int d, int with_weights) {
     DecodePlan w;
     const int group = H / H_kv;
+    // up to 16 query heads a row, which unpacks the keys once for them; by 8 where there are not more (us 16 / by 8 of
+    // 16 heads a key, d 128, bf16, caches of 8192: 64 x 4 rows 162 / 207, 16 x 2 rows 43 / 41, one row 31 / 18)
     w.nt = group > 8 ? 2 : 1;
     w.head_blocks = (group + 8 * w.nt - 1) / (8 * w.nt);
     const long rows = (long)B * H_kv * w.head_blocks;
@@ -381,9 +383,10 @@ la_status la_kv4_evict(const la_kv4_cache *cache, const float *weights, const in
     p.recent = recent; p.out_weights = out_weights; p.kept = kept; p.out_lens = out_lens;
     p.list = kept ? kept : (int32_t *)workspace;
     cudaStream_t st = (cudaStream_t)stream;
-    // short caches: small blocks, whose barriers are cheaper; long ones: as many CTAs
-    // of a (sequence, head) as its positions fill with 8 keys a thread and the
-    // machine has SMs for
+    // Short caches: blocks of 256 threads, whose barriers are cheaper and of which several fit an SM; long ones: of
+    // 1024, as many CTAs of a (sequence, head) as its positions fill with 8 keys a thread and the machine has SMs for
+    // (us 256 / 1024 threads, cut to half, d 128: 2 rows 12 / 14 at 400 positions, 16 / 16 at 1024, 22 / 22 at 2048;
+    // 296 rows 16 / 29, 25 / 35, 39 / 47; d 64, 2 rows 43 / 24 at 4096, 80 / 31 at 8192)
     const long rows = (long)cache->B * cache->H_kv;
     if (cache->cap <= 256 * kEvictKeys) return run_evict<256>(p, cache->d, rows, 1, st);
     int cs = 1;

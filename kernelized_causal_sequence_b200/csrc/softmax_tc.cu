@@ -62,11 +62,11 @@ la_status run(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned
 }
 
 // Which slots (us, 16 query heads; one tile / two slots; S sequences of L tokens):
-//   d 128, 4 key heads   64 x 200: 62 / 59, 32 x 512: 82 / 77, 16 x 1000: 111 / 103, 8 x 2048: 164 / 150, 1 x 8192: 258 / 242
-//   d 128, 16 key heads  64 x 200: 66 / 67, 32 x 512: 85 / 83, 16 x 1000: 114 / 107, 8 x 2048: 170 / 156, 1 x 8192: 269 / 268
-//   d 128, 1 x 4096      78 / 75 and 78 / 77; 1 x 2048: 40 / 42 and 40 / 43 (too few tiles of two slots)
-//   d 64                 one tile up to 8192 tokens (1 x 8192: 200 / 209): the softmax bounds it there
-// Two slots read a key and value tile once for both, which counts where the
+//   d 128, 4 key heads   64 x 200: 66 / 62, 32 x 512: 84 / 80, 16 x 1000: 112 / 105, 8 x 2048: 168 / 155, 1 x 8192: 266 / 251
+//   d 128, 16 key heads  64 x 200: 64 / 66, 32 x 512: 86 / 85, 16 x 1000: 117 / 110, 8 x 2048: 175 / 160, 1 x 8192: 275 / 258
+//   d 128, 1 x 4096      80 / 78 and 82 / 80; 1 x 2048: 41 / 43 and 41 / 45 (too few tiles of two slots)
+//   d 64                 one tile up to 8192 tokens (1 x 8192: 200 / 209 when two were built): the softmax bounds it there
+// (N stands for the lengths, which are on the device; a buffer longer than its batch counts as longer sequences.)  Two slots read a key and value tile once for both, which counts where the
 // products' operands bound it; one tile leaves less empty and more to overlap.
 template <typename InT, typename OutT, int D>
 la_status by_slots(const SoftmaxParams &sp, la_dtype dt, int d, int *status, unsigned long long wait_ns, cudaStream_t st) {

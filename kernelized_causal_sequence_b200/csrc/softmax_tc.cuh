@@ -24,8 +24,8 @@
 // The two slots (or two CTAs of one) alternate on the tensor core: while one
 // slot's exponentials run, the products of the other do.
 //
-// What bounds it.  d 128, 16384 tokens, 16 heads on 2: 896 us, 1.2 PFLOP/s.  Measured
-// when it took 910: the tensor pipe active 51% of the time; without the
+// What bounds it.  d 128, 16384 tokens, 16 heads on 2: 917 us, 1.2 PFLOP/s (1058 among
+// other calls).  Measured when it took 910: the tensor pipe active 51% of the time; without the
 // exponentials 894 us, without maximum and sum too 891, with half the products
 // 784, with an eighth of the products and none of that arithmetic 513.  So it is
 // neither the products nor the arithmetic alone, but the chain S -> TMEM load ->
@@ -35,7 +35,7 @@
 // chain and were slower, 1156 us for 910: a product with N = 64 reads Q as often
 // as one with 128.  P handed over in halves, so that its first product runs under
 // the second half's exponentials, was slower too (912 for 896).  d 64, 32 prompts
-// up to 700 tokens: 45 us, of which copies and the first products before any
+// up to 700 tokens: 46 us, of which copies and the first products before any
 // softmax are a good part; for long prompts the softmax is the bound (226 us with,
 // 170 us without it when this was tried: 8192 tokens, 16 heads; 200 us now).
 // Computing part of the exponentials on the FMA units gained nothing: a warp's
@@ -307,7 +307,7 @@ softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // one slot 128 x 200 + 128 x 56, of the 384 x 168 of two slots 256 x 216 +
     // 128 x 56 (never more than the CTA was launched with: an increase would wait
     // for good).  With 168 for all, two slots took 917 us for 896 (16384 tokens,
-    // 16 heads on 2) and 317 for 304 (eight packed prompts).
+    // 16 heads on 2) and 317 for 304 (eight packed prompts) when this was tried.
     if (warp >= G::TMA_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == G::TMA_WARP) {
