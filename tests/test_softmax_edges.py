@@ -343,3 +343,67 @@ def test_evict_without_optional_outputs(la, cap, lens, keep, recent):
         for i, y in enumerate((kept, ow, ol)):
             if asked >> i & 1:
                 assert torch.equal(got[i], y)
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.gpu
+def test_calls_at_once(la):
+    """Prompts of both kinds of CTA, a decode and an eviction on streams of their own, with workspaces of their own, and
+    the same calls replayed from one captured graph after their inputs changed: the bits of the calls one by one."""
+    lens = [700, 1300, 64, 257]
+    a = [x.to(DEV) for x in prefill_inputs(torch.float16, 64, 8, 8, sum(lens), seed=41)]
+    b = [x.to(DEV) for x in prefill_inputs(torch.bfloat16, 128, 32, 16, sum(lens), seed=42)]
+    cu = cu_of(lens)
+    g = torch.Generator().manual_seed(43)
+    k, v = torch.randn(4, 2, 1500, 64, generator=g), torch.randn(4, 2, 1500, 64, generator=g)
+    cache, _, _ = fill_cache(la, k, v)
+    cap = cache.k_codes.shape[2]
+    q = torch.randn(4, 8, 64, generator=g).to(torch.bfloat16).to(DEV)
+    tl, w = i32(1500, 3, 0, 900), torch.rand(4, 2, cap, generator=g).to(DEV)
+    need = [la.la_softmax_prefill_workspace_size(8, 8, sum(lens), 64, 4), la.la_softmax_prefill_workspace_size(32, 16, sum(lens), 128, 4),
+            la.la_kv4_decode_workspace_size(4, 8, 2, cap, 64, True)]
+    ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in need]
+    out = [torch.zeros_like(a[0]), torch.zeros_like(b[0]), torch.zeros_like(q), torch.zeros_like(w)]
+    small = la.KV4Cache.alloc(4, 2, 300, 64, DEV)
+    ow = torch.zeros(4, 2, 300, device=DEV)
+    calls = [lambda: la.la_softmax_prefill(*a, cu, out=out[0], workspace=ws[0]),
+             lambda: la.la_softmax_prefill(*b, cu, out=out[1], workspace=ws[1]),
+             lambda: la.la_kv4_decode(q, cache, tl, weights_in=w, weights_out=out[3], out=out[2], workspace=ws[2]),
+             lambda: la.la_kv4_evict(cache, w, tl, 300, recent=20, out=small, out_weights=ow)]
+
+    def results():
+        torch.cuda.synchronize()
+        x = [t.clone() for t in (*out, ow)] + [small.k_codes[0].clone(), small.v_par[0].clone()]
+        for t in (*out, ow):
+            t.zero_()
+        return x
+
+    def same(x, y):
+        return all(torch.equal(s, t) for s, t in zip(x, y))
+    for call in calls:
+        call()
+    want = results()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        torch.cuda.synchronize()
+        for call, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                call()
+        assert same(results(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in calls:
+            call()
+    graph.replay()
+    assert same(results(), want)
+    cu.copy_(cu_of([1, 0, 1500, 600]))
+    tl.copy_(i32(0, 1400, 299, 301))
+    q.mul_(-1)
+    graph.replay()
+    got = results()
+    for call in calls:
+        call()
+    again = results()
+    assert same(got, again) and not same(got, want)
+    for x in ws[:2]:
+        assert la.la_workspace_status(x) == (la.LA_OK, 0)
